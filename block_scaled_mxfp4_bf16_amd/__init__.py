@@ -61,6 +61,7 @@ def _load():
         "mxfp4_set_quant_mode": (I, [I]),
         "mxfp4_set_schedule_override": (I, [ctypes.c_char_p]),
         "mxfp4_list_schedules": (SZ, [I64, I64, I64, I, ctypes.c_char_p, SZ]),
+        "mxfp4_gemv": (I, [P, I, I64, P, P, P, I64, P, I, I64, I64, I64, I64, I64, I, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -79,7 +80,8 @@ def exported_symbols():
     return ["mxfp4_packed_bytes", "mxfp4_raw_scale_bytes", "mxfp4_shuffled_scale_bytes",
             "mxfp4_gemm_workspace_bytes", "mxfp4_quantize", "mxfp4_preshuffle_b", "mxfp4_prepare_b", "mxfp4_gemm",
             "mxfp4_gemm_ex", "mxfp4_gemm_noalloc", "mxfp4_gemm_q", "mxfp4_gemm_q_schedule_name", "mxfp4_reserve", "mxfp4_status_string", "mxfp4_last_hip_error", "mxfp4_gemm_schedule_name",
-            "mxfp4_set_quant_mode", "mxfp4_set_schedule_override", "mxfp4_list_schedules"]
+            "mxfp4_set_quant_mode", "mxfp4_set_schedule_override", "mxfp4_list_schedules",
+            "mxfp4_gemv"]
 
 
 def _check(rc: int, what: str):
@@ -196,6 +198,12 @@ def mxfp4_list_schedules(M: int, N: int, K: int, quantized_a: bool = False):
     return buf.value.decode().split()
 
 
+def mxfp4_gemv(x, x_type: int, ldx: int, Bq_sh, Bs_sh, ids, experts: int, y, y_type: int, ldy: int, M: int, N: int,
+               K: int, repeat: int = 1, gated: bool = False, stream=None):
+    _check(_load().mxfp4_gemv(_ptr(x), x_type, ldx, _ptr(Bq_sh), _ptr(Bs_sh), _ptr(ids), experts, _ptr(y), y_type, ldy,
+                              M, N, K, repeat, int(bool(gated)), _stream(stream)), "mxfp4_gemv")
+
+
 # ---- tensor conveniences (allocate outputs with torch, then call the above) --
 
 def quantize(x, shuffled_scales: bool = False, stream=None):
@@ -255,4 +263,88 @@ def gemm(A, Bw, Bs, N: int, out=None, stream=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
     mxfp4_gemm(A, Bw, Bs, out, M, N, K, stream)
+    return out
+
+
+# ---- expert operators --------------------------------------------------------
+
+MXFP4_TYPE_BF16, MXFP4_TYPE_F16, MXFP4_TYPE_F32 = 0, 1, 2
+
+_types = {}
+
+
+def _type(t):
+    """MXFP4_TYPE_* of a tensor's dtype."""
+    if not _types:
+        import torch
+        _types.update({torch.bfloat16: MXFP4_TYPE_BF16, torch.float16: MXFP4_TYPE_F16, torch.float32: MXFP4_TYPE_F32})
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        raise TypeError("expected a bf16, f16 or f32 tensor, got %s" % t.dtype) from None
+
+
+def _int32(t, what, n, like):
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n or t.device != like.device:
+        raise ValueError("%s must be a contiguous int32 tensor of %d elements on %s" % (what, n, like.device))
+
+
+def _rows_of(t, what, rows, cols, like):
+    """Checks a [rows, cols] tensor whose rows are contiguous; rows may be None."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != cols or t.device != like.device \
+            or (cols > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a [%s, %d] tensor on %s with contiguous rows" %
+                         (what, "rows" if rows is None else rows, cols, like.device))
+
+
+def _prepared(Bw, Bs, N, K, like):
+    """Number of matrices in prepared codes and scales; checks their sizes."""
+    per_w, per_s = mxfp4_packed_bytes(N, K), mxfp4_shuffled_scale_bytes(N, K)
+    E = Bw.numel() // per_w if per_w else 0
+    if E < 1 or Bw.numel() != E * per_w or Bs.numel() != E * per_s or Bw.element_size() != 1 or Bs.element_size() != 1 \
+            or not Bw.is_contiguous() or not Bs.is_contiguous() or Bw.device != like.device or Bs.device != like.device:
+        raise ValueError("Bw and Bs must be contiguous byte tensors of prepared [%d, %d] matrices on %s" %
+                         (N, K, like.device))
+    return E
+
+
+def prepare_experts(B, stream=None):
+    """bf16 [E, N, K] cuda tensor -> (Bw [E, N/16, (K/2)*16], Bs [E, ...]): each matrix prepared as by prepare_b."""
+    import torch
+    E, N, K = B.shape
+    assert B.dtype == torch.bfloat16 and B.is_contiguous()
+    bw = torch.empty((E, N // 16, (K // 2) * 16), dtype=torch.uint8, device=B.device)
+    bs = torch.empty(E * mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=B.device)
+    bs = bs.view(E, -1, ((K // 32 + 7) // 8) * 32)
+    for e in range(E):
+        mxfp4_prepare_b(B[e], N, K, bw[e], bs[e], stream)
+    return bw, bs
+
+
+def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=None, out_dtype=None, stream=None):
+    """y = x * B^T for few rows of unquantized bf16, f16 or f32 activations.
+
+    x [M, K] with contiguous rows; Bw, Bs from prepare_b.  With ids (int32,
+    one per row of y) Bw and Bs hold several matrices (prepare_experts), row r
+    of y takes matrix ids[r] and row r // repeat of x, and a row whose id is
+    none of them is zero.  gated: N/2 columns, silu(first half) * second.
+    y's type is out's, else out_dtype, else x's."""
+    import torch
+    K = x.shape[1]
+    _rows_of(x, "x", None, K, x)
+    xt = _type(x)
+    E = _prepared(Bw, Bs, N, K, x)
+    M = x.shape[0] * repeat
+    if ids is not None:
+        _int32(ids, "ids", M, x)
+    elif E != 1:
+        raise ValueError("%d matrices need ids" % E)
+    cols = N // 2 if gated else N
+    if out is None:
+        out = torch.empty((M, cols), dtype=out_dtype or x.dtype, device=x.device)
+    else:
+        _rows_of(out, "out", M, cols, x)
+    mxfp4_gemv(x, xt, x.stride(0) if x.shape[0] > 1 else K, Bw, Bs, ids, E, out, _type(out),
+               out.stride(0) if M > 1 else cols, M, N, K, repeat, gated, stream)
     return out

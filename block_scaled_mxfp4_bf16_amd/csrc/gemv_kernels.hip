@@ -1,0 +1,334 @@
+// Products of a few rows with MXFP4 weights, the activations unquantized:
+//   y[r, n] = sum_k x[r, k] * e2m1(code[n, k]) * 2^(s[n, k / 32] - 127)
+// and its gated form, silu(first half of the columns) * (second half).
+//
+// Reading the weights bounds it: N * K * 17/32 bytes against 2 * M * N * K
+// flops.  A wave takes 16 columns x 128 elements of K at a time, one 16-byte
+// load per lane (the prepared layout makes that 1 KiB contiguous), converts
+// the codes to 16-bit floats with the hardware's scaled convert and feeds
+// the 16x16x32 matrix instruction, whose 16 rows serve every M up to 16 at
+// the same price.  The converts (16 per KiB) and the products (4 per KiB)
+// leave the vector units idle most of the time at the rate that memory
+// delivers, so there is nothing to win from a separate dot-product form for
+// one row.
+//
+// Lane l of the load holds column l % 16 and group 4 * step + l / 16: all 32
+// elements of one group, so one scale per lane.
+//   bf16 rows  the convert applies the scale: e2m1 * 2^e is exact in bf16.
+//              Product i takes elements 8i..8i+7 of the lane's group.
+//   f32 rows   as bf16, with x cut into three bf16 parts of 8 significand
+//              bits each: hi + mid + lo = x exactly, so the only rounding is
+//              that of the f32 sums, as in a product of f32 by f32.
+//   f16 rows   a scaled weight may leave f16's range, so the codes are
+//              converted unscaled and the f32 sum of each group is scaled
+//              instead.  That needs products that stay within one group: the
+//              four dwords of the lanes of a column are transposed over the
+//              four lane quarters with two kinds of lane swaps, after which
+//              product i takes the whole of group 4 * step + i.
+// The waves of a workgroup split K and add their tiles through LDS in wave
+// order; sums are f32, rounded once to y's type.
+#include "experts_device.hpp"
+#include "experts_internal.hpp"
+
+namespace mxfp4 {
+
+namespace {
+
+enum { kBf16 = 0, kF16 = 1, kF32 = 2 };
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+// Eight weights of one dword of codes as bf16, scaled by a power of two.
+__device__ __forceinline__ bf16x8 weights_bf16(uint32_t w, float scale) {
+  union {
+    bf16x2 h[4];
+    bf16x8 v;
+  } u;
+  u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+  u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+  u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  return u.v;
+}
+
+__device__ __forceinline__ f16x8 weights_f16(uint32_t w) {
+  union {
+    f16x2 h[4];
+    f16x8 v;
+  } u;
+  u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+  u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+  u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+  u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+  return u.v;
+}
+
+// Swap the upper 32 lanes of a with the lower 32 of b.
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r.x;
+  b = r.y;
+}
+// Swap lanes 16-31 of a with lanes 0-15 of b, and 48-63 with 32-47.
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r.x;
+  b = r.y;
+}
+
+// Eight f32 values as three bf16 vectors whose sum is exact: each part is
+// the top 16 bits of what the parts before it left.  Infinities and NaN stay
+// in the first part (inf - inf would make them NaN).
+__device__ __forceinline__ void split_f32(const u32x4 &p, const u32x4 &q, bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+  const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+  uint32_t h[8], m[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // a NaN whose payload sits in the low half keeps its quiet bit
+    const bool special = (v[i] & 0x7F800000u) == 0x7F800000u;
+    const uint32_t keep = special && (v[i] & 0x007FFFFFu) ? 0x00400000u : 0u;
+    h[i] = v[i] | keep;
+    const float r = special ? 0.0f : __uint_as_float(v[i]) - __uint_as_float(v[i] & 0xFFFF0000u);
+    m[i] = __float_as_uint(r);
+    l[i] = __float_as_uint(r - __uint_as_float(m[i] & 0xFFFF0000u));
+  }
+  union {
+    uint32_t u[4];
+    bf16x8 v;
+  } a, b, c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a.u[i] = (h[2 * i] >> 16) | (h[2 * i + 1] & 0xFFFF0000u);
+    b.u[i] = (m[2 * i] >> 16) | (m[2 * i + 1] & 0xFFFF0000u);
+    c.u[i] = (l[2 * i] >> 16) | (l[2 * i + 1] & 0xFFFF0000u);
+  }
+  hi = a.v;
+  mid = b.v;
+  lo = c.v;
+}
+
+}  // namespace
+
+// Workgroup: 16*MT rows (or, with ids, one row) x 16*NT columns, all of K;
+// wave w takes steps w, w + WK, ... with D steps in flight.  With `gated`
+// the first NT/2 subtiles are gate columns and the others their up columns.
+template <int XT, int MT, int NT, int WK, int D>
+__global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
+  constexpr int XL = XT == kF32 ? 8 : 4;  // 16-byte loads of x per row tile and step
+  constexpr int ES = XT == kF32 ? 4 : 2;  // bytes per element of x
+  constexpr int NSD = NT > 1 ? NT : 1;
+  __shared__ __attribute__((aligned(16))) float red[WK * MT * NT * 256];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n16 = lane & 15, q4 = lane >> 4;
+  const int N = a.N, K = a.K;
+  const int KS = (K + 127) >> 7;
+  const int G = K >> 5;
+  const int gp = (G + 7) & ~7;
+
+  int row0 = blockIdx.y * 16 * MT, rows = a.M - row0;
+  int64_t xrow = row0;
+  const uint8_t *Bw = a.Bw, *Bs = a.Bs;
+  const int out_cols = a.gated ? N >> 1 : N;
+  const int cols = a.gated ? 8 * NT : 16 * NT;  // output columns of this workgroup
+  const int b_bytes = (N >> 4) * K * 8;
+  const int s_bytes = ((N + 255) >> 8) * 8 * gp * 32;
+  bool live = true;
+  if (a.ids) {
+    row0 = blockIdx.y;
+    rows = 1;
+    xrow = row0 / a.repeat;
+    const int id = __builtin_amdgcn_readfirstlane(a.ids[row0]);
+    live = id >= 0 && id < a.experts;
+    const int64_t e = live ? id : 0;
+    Bw += e * b_bytes;
+    Bs += e * s_bytes;
+  }
+  if (rows > 16 * MT) rows = 16 * MT;
+
+  const uint8_t *x = (const uint8_t *)a.x + xrow * a.ldx * ES;
+  const int ldx = (int)a.ldx * ES;
+  const int x_bytes = (rows - 1) * ldx + K * ES;
+  const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)x, 0, x_bytes, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)Bw, 0, b_bytes, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)Bs, 0, s_bytes, kRsrcWord3);
+
+  // 16-row groups of B this workgroup reads; groups past N (the last
+  // workgroup of an N that is no multiple of the tile) load zeros
+  const int groups = N >> 4;
+  const int first = blockIdx.x * (cols >> 4);
+  int gw[NT];
+  bool gok[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (a.gated) {
+      const int c = first + (nt % (NT > 1 ? NT / 2 : 1));
+      gok[nt] = c < (groups >> 1);
+      gw[nt] = nt < NT / 2 ? c : (groups >> 1) + c;
+    } else {
+      gw[nt] = first + nt;
+      gok[nt] = gw[nt] < groups;
+    }
+  }
+
+  struct Stage {
+    u32x4 x[MT][XL];
+    u32x4 b[NT];
+    uint32_t s[NSD];
+  };
+  const int steps = live ? KS : 0;
+  auto load = [&](int ks, Stage &st) {
+    const bool ok = ks < steps;
+    const bool bk = ok && 4 * ks + q4 < G;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      st.b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
+          b_rsrc, off_or_oob(bk && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
+      st.s[nt] = __builtin_amdgcn_raw_buffer_load_b32(
+          s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = 16 * mt + n16;
+#pragma unroll
+      for (int i = 0; i < XL; ++i) {
+        // first element of the 16 bytes, in the order the products take them
+        const int el = XT == kF16 ? i * 32 + q4 * 8 : q4 * 32 + i * (16 / ES);
+        const int g = 4 * ks + (XT == kF16 ? i : q4);
+        st.x[mt][i] = __builtin_amdgcn_raw_buffer_load_b128(
+            x_rsrc, off_or_oob(ok && r < rows && g < G, r * ldx + (ks * 128 + el) * ES), 0, 0);
+      }
+    }
+  };
+
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](int ks, const Stage &st) {
+    bf16x8 part[MT][XT == kF32 ? 3 : 1][4];
+    if constexpr (XT == kF32) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          split_f32(st.x[mt][2 * i], st.x[mt][2 * i + 1], part[mt][0][i], part[mt][1][i], part[mt][2][i]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      // byte (row block half) + 2 * (step parity) of the scale dword
+      const uint32_t sbits = ((st.s[nt] >> (8 * ((gw[nt] & 1) + 2 * (ks & 1)))) & 0xFFu) << 23;
+      if constexpr (XT == kF16) {
+        uint32_t d0 = st.b[nt].x, d1 = st.b[nt].y, d2 = st.b[nt].z, d3 = st.b[nt].w;
+        swap32(d0, d2);
+        swap32(d1, d3);
+        swap16(d0, d1);
+        swap16(d2, d3);
+        // the four groups' scales, each in every lane of its column
+        uint32_t s0 = sbits, s2 = sbits;
+        swap32(s0, s2);
+        uint32_t s1 = s0, s3 = s2;
+        swap16(s0, s1);
+        swap16(s2, s3);
+        const uint32_t d[4] = {d0, d1, d2, d3};
+        const uint32_t s[4] = {s0, s1, s2, s3};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f16x8 w = weights_f16(d[i]);
+          // scale byte 0 stands for 2^-127
+          const float sc = s[i] ? __uint_as_float(s[i]) : __uint_as_float(0x00400000u);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, st.x[mt][i]), w,
+                                                                 v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[mt][nt][r] += p[r] * sc;
+          }
+        }
+      } else {
+        const float sc = __uint_as_float(sbits);
+        const uint32_t d[4] = {st.b[nt].x, st.b[nt].y, st.b[nt].z, st.b[nt].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8 w = weights_bf16(d[i], sc);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if constexpr (XT == kF32) {
+#pragma unroll
+              for (int h = 2; h >= 0; --h)
+                acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[mt][h][i], w, acc[mt][nt], 0, 0, 0);
+            } else {
+              acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x[mt][i]), w,
+                                                                    acc[mt][nt], 0, 0, 0);
+            }
+          }
+        }
+      }
+    }
+  };
+
+  // Steps past K load zeros and add nothing, so the loop has no branch
+  // between a load and its use.
+  Stage st[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(wave + WK * d, st[d]);
+  const int rounds = (KS + WK * D - 1) / (WK * D);
+  for (int it = 0; it < rounds; ++it) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      compute(wave + WK * (it * D + d), st[d]);
+      load(wave + WK * ((it + 1) * D + d), st[d]);
+    }
+  }
+
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (16 * mt + 4 * q4 + r < rows) red[((wave * MT + mt) * NT + nt) * 256 + r * 64 + lane] = acc[mt][nt][r];
+  __syncthreads();
+  auto sum = [&](int row, int nt, int n) {
+    const int at = ((row >> 4) * NT + nt) * 256 + (row & 3) * 64 + ((row >> 2) & 3) * 16 + n;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) v += red[w * MT * NT * 256 + at];
+    return v;
+  };
+  for (int j = threadIdx.x; j < rows * cols; j += 64 * WK) {
+    const int row = j / cols, c = j - row * cols;
+    const int col = blockIdx.x * cols + c;
+    if (col >= out_cols) continue;
+    float v = sum(row, c >> 4, c & 15);
+    if (a.gated) v = gated_silu(v, sum(row, NT / 2 + (c >> 4), c & 15));
+    store_as(a.y, a.y_type, (size_t)(row0 + row) * a.ldy + col, v);
+  }
+}
+
+template <int XT, int MT, int NT, int WK, int D>
+static hipError_t run_gemv(const GemvArgs &a, hipStream_t stream) {
+  const int cols = a.gated ? 8 * NT : 16 * NT;
+  const int out_cols = a.gated ? a.N >> 1 : a.N;
+  const dim3 grid((out_cols + cols - 1) / cols, a.ids ? a.M : (a.M + 16 * MT - 1) / (16 * MT));
+  gemv_kernel<XT, MT, NT, WK, D><<<grid, 64 * WK, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int XT>
+static hipError_t run_gemv_rows(const GemvArgs &a, hipStream_t stream) {
+  if (a.ids || a.M <= 16) return run_gemv<XT, 1, 2, 8, 2>(a, stream);
+  if (a.M <= 32) return run_gemv<XT, 2, 2, 8, 2>(a, stream);
+  return run_gemv<XT, 4, 2, 8, 1>(a, stream);
+}
+
+hipError_t launch_gemv(const GemvArgs &a, hipStream_t stream) {
+  if (a.x_type == kF16) return run_gemv_rows<kF16>(a, stream);
+  if (a.x_type == kF32) return run_gemv_rows<kF32>(a, stream);
+  return run_gemv_rows<kBf16>(a, stream);
+}
+
+}  // namespace mxfp4

@@ -24,11 +24,19 @@ const int64_t kMaxBytes = (int64_t)1 << 31;  // 32-bit offsets inside the kernel
 // The last HIP error this thread's calls into the library met.
 thread_local hipError_t t_last_hip_error = hipSuccess;
 
+}  // namespace
+
+namespace mxfp4 {
+
 mxfp4_status_t hip_status(hipError_t e) {
   if (e == hipSuccess) return MXFP4_OK;
   t_last_hip_error = e;
   return MXFP4_ERR_HIP;
 }
+
+}  // namespace mxfp4
+
+namespace {
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -357,6 +365,10 @@ int alloc_workspace(int device, void *stream, size_t bytes, void **out) {
 
 WorkspacePool<int (*)(int, void *, size_t, void **)> g_ws(alloc_workspace);
 
+}  // namespace
+
+namespace mxfp4 {
+
 mxfp4_status_t get_workspace(size_t need, hipStream_t stream, void **out) {
   *out = nullptr;
   if (need == 0) return MXFP4_OK;
@@ -364,6 +376,10 @@ mxfp4_status_t get_workspace(size_t need, hipStream_t stream, void **out) {
   if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
   return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, out);
 }
+
+}  // namespace mxfp4
+
+namespace {
 
 // Scratch of mxfp4_gemm_noalloc: a file-scope device array, one copy per
 // GPU, held until the process ends.  Host code never uses its name as an
@@ -395,12 +411,16 @@ mxfp4_status_t scratch_of_current_device(hipStream_t stream, void **out) {
   return MXFP4_OK;
 }
 
+}  // namespace
+
+namespace mxfp4 {
+
 bool sw_quant() {
   std::lock_guard<std::mutex> lk(g_opt_mu);
   return g_quant_mode == 1;
 }
 
-}  // namespace
+}  // namespace mxfp4
 
 extern "C" {
 

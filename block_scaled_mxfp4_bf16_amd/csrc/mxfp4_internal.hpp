@@ -5,7 +5,16 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/mxfp4.h"
+
 namespace mxfp4 {
+
+// Shared by the files that hold entry points (mxfp4_api.hip): the status of
+// a HIP call, the library-owned workspace of (current device, stream), and
+// the encoder mode.
+mxfp4_status_t hip_status(hipError_t e);
+mxfp4_status_t get_workspace(size_t need, hipStream_t stream, void **out);
+bool sw_quant();
 
 // A GEMM schedule: compile-time tile shape plus the runtime split count.
 //   mt    16-row M tiles per workgroup (the workgroup covers 16*mt rows)

@@ -283,6 +283,41 @@ MXFP4_API mxfp4_status_t mxfp4_set_schedule_override(const char *name);
  * Returns 0 for a shape outside the ABI (see mxfp4_gemm's errors). */
 MXFP4_API size_t mxfp4_list_schedules(int64_t M, int64_t N, int64_t K, int quantized_a, char *buf, size_t cap);
 
+/* ------------------------------------------------------------------------ */
+/* Expert operators: what a mixture-of-experts block needs around the GEMM.  */
+/* The E weight matrices of a block lie one behind the other, each prepared  */
+/* as for mxfp4_gemm: codes at e * mxfp4_packed_bytes(N, K), scales at       */
+/* e * mxfp4_shuffled_scale_bytes(N, K).                                     */
+/* "Gated" products have a weight matrix whose first N/2 rows are the gate   */
+/* and the last N/2 the up projection, and return N/2 columns,               */
+/* silu(gate) * up with silu(v) = v / (1 + exp(-v)), formed from the f32     */
+/* sums before anything is rounded.                                          */
+/* ------------------------------------------------------------------------ */
+typedef enum { MXFP4_TYPE_BF16 = 0, MXFP4_TYPE_F16 = 1, MXFP4_TYPE_F32 = 2 } mxfp4_type_t;
+
+/* Products of a few rows with MXFP4 weights, the activations unquantized:   */
+/*   y[r, n] = sum_k x[r, k] * B[n, k]                 (ids == NULL)          */
+/*   y[r, n] = sum_k x[r / repeat, k] * B_ids[r][n, k]  (ids != NULL)         */
+/* The weights are exact, the sums f32 in a fixed order, rounded once to y's */
+/* type.  Made for single tokens and small batches, whose time is that of    */
+/* reading B; any M is right.                                                */
+/*   x       rows of K elements of x_type, ldx elements apart       (input)   */
+/*   Bq_sh, Bs_sh  one prepared matrix, or `experts` of them        (input)   */
+/*   ids     int32 [M]: the matrix of each row; a row whose id is outside    */
+/*           [0, experts) is set to zero.  NULL: one matrix for all (input)   */
+/*   y       [M, N] (gated: [M, N/2]) of y_type, ldy elements apart (output)  */
+/*   repeat  rows of y per row of x (a token's experts); 1 without ids       */
+/* A row of NaN or Inf touches its own row of y only.                        */
+/* Errors: INVALID_ARG (null, M, N, K, experts or repeat < 1, repeat != 1    */
+/*         without ids, unknown type, ldx < K or ldy < y's columns, x or its */
+/*         row stride not 16-byte aligned, B not 16-byte aligned, y not       */
+/*         aligned to its type);                                             */
+/*         UNSUPPORTED (K % 32 != 0, N % 16 != 0, gated with N % 32 != 0,    */
+/*         a matrix or 64 rows of x beyond 2^31 bytes, M beyond 2^20 rows).  */
+MXFP4_API mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, const void *Bq_sh, const void *Bs_sh,
+                                    const int32_t *ids, int64_t experts, void *y, int y_type, int64_t ldy, int64_t M,
+                                    int64_t N, int64_t K, int64_t repeat, int gated, mxfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
