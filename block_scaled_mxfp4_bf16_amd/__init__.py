@@ -62,6 +62,10 @@ def _load():
         "mxfp4_set_schedule_override": (I, [ctypes.c_char_p]),
         "mxfp4_list_schedules": (SZ, [I64, I64, I64, I, ctypes.c_char_p, SZ]),
         "mxfp4_gemv": (I, [P, I, I64, P, P, P, I64, P, I, I64, I64, I64, I64, I64, I, P]),
+        "mxfp4_reserve_bytes": (I, [SZ, P]),
+        "mxfp4_moe_route_workspace_bytes": (SZ, [I64, I64]),
+        "mxfp4_moe_route": (I, [P, I, I64, P, I64, I64, I64, I, I, P, P, P, P, P, P, SZ, P]),
+        "mxfp4_moe_combine": (I, [P, I, I64, I64, P, P, P, I64, P, I, I64, I64, I64, I64, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -81,7 +85,8 @@ def exported_symbols():
             "mxfp4_gemm_workspace_bytes", "mxfp4_quantize", "mxfp4_preshuffle_b", "mxfp4_prepare_b", "mxfp4_gemm",
             "mxfp4_gemm_ex", "mxfp4_gemm_noalloc", "mxfp4_gemm_q", "mxfp4_gemm_q_schedule_name", "mxfp4_reserve", "mxfp4_status_string", "mxfp4_last_hip_error", "mxfp4_gemm_schedule_name",
             "mxfp4_set_quant_mode", "mxfp4_set_schedule_override", "mxfp4_list_schedules",
-            "mxfp4_gemv"]
+            "mxfp4_gemv", "mxfp4_reserve_bytes", "mxfp4_moe_route_workspace_bytes", "mxfp4_moe_route",
+            "mxfp4_moe_combine"]
 
 
 def _check(rc: int, what: str):
@@ -204,6 +209,27 @@ def mxfp4_gemv(x, x_type: int, ldx: int, Bq_sh, Bs_sh, ids, experts: int, y, y_t
                               M, N, K, repeat, int(bool(gated)), _stream(stream)), "mxfp4_gemv")
 
 
+def mxfp4_reserve_bytes(nbytes: int, stream=None):
+    _check(_load().mxfp4_reserve_bytes(nbytes, _stream(stream)), "mxfp4_reserve_bytes")
+
+
+def mxfp4_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return _load().mxfp4_moe_route_workspace_bytes(T, E)
+
+
+def mxfp4_moe_route(logits, x_type: int, ld: int, bias, T: int, E: int, k: int, score: int, renormalize: bool, ids,
+                    weights, offsets, rows, pos, workspace=None, workspace_bytes: int = 0, stream=None):
+    _check(_load().mxfp4_moe_route(_ptr(logits), x_type, ld, _ptr(bias), T, E, k, score, int(bool(renormalize)),
+                                   _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(rows), _ptr(pos), _ptr(workspace),
+                                   workspace_bytes, _stream(stream)), "mxfp4_moe_route")
+
+
+def mxfp4_moe_combine(y, y_type: int, ld_y: int, rows: int, weights, pos, residual, ld_res: int, out, out_type: int,
+                      ld_out: int, T: int, k: int, N: int, stream=None):
+    _check(_load().mxfp4_moe_combine(_ptr(y), y_type, ld_y, rows, _ptr(weights), _ptr(pos), _ptr(residual), ld_res,
+                                     _ptr(out), out_type, ld_out, T, k, N, _stream(stream)), "mxfp4_moe_combine")
+
+
 # ---- tensor conveniences (allocate outputs with torch, then call the above) --
 
 def quantize(x, shuffled_scales: bool = False, stream=None):
@@ -309,6 +335,11 @@ def _prepared(Bw, Bs, N, K, like):
     return E
 
 
+def _on_gpu(t):
+    if not t.is_cuda:
+        raise ValueError("the expert operators take cuda tensors, not %s ones" % t.device)
+
+
 def prepare_experts(B, stream=None):
     """bf16 [E, N, K] cuda tensor -> (Bw [E, N/16, (K/2)*16], Bs [E, ...]): each matrix prepared as by prepare_b."""
     import torch
@@ -345,6 +376,93 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
         out = torch.empty((M, cols), dtype=out_dtype or x.dtype, device=x.device)
     else:
         _rows_of(out, "out", M, cols, x)
+    _on_gpu(x)
+    if M == 0:
+        return out
     mxfp4_gemv(x, xt, x.stride(0) if x.shape[0] > 1 else K, Bw, Bs, ids, E, out, _type(out),
                out.stride(0) if M > 1 else cols, M, N, K, repeat, gated, stream)
+    return out
+
+
+_scores = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bool = True, out=None, stream=None):
+    """The k experts of each token and the (token, choice) pairs sorted by expert.
+
+    logits [T, E], bf16, f16 or f32, with contiguous rows; score "softmax" or
+    "sigmoid" gives g; the experts of the largest g (+ bias, f32 [E]) are
+    chosen, never one whose logit or bias is -inf or NaN.  Returns (or fills,
+    if given as out):
+      ids     int32 [T, k], -1 where no expert was left
+      weights f32 [T, k], g of the chosen, renormalized to sum 1 if asked
+      offsets int32 [E + 1], where each expert's pairs lie in rows
+      rows    int32 [T * k], the pair t * k + j at each sorted place, or -1
+      pos     int32 [T, k], the sorted place of each pair, or -1"""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    _rows_of(logits, "logits", T, E, logits)
+    lt = _type(logits)
+    if score not in _scores:
+        raise ValueError("score must be 'softmax' or 'sigmoid', not %r" % (score,))
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous()
+                             or bias.device != logits.device):
+        raise ValueError("bias must be a contiguous f32 tensor of %d elements on %s" % (E, logits.device))
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=logits.device)
+        out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=logits.device),
+               torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32))
+    else:
+        ids, weights, offsets, rows, pos = out
+        _int32(ids, "ids", T * k, logits)
+        _weights(weights, T, k, logits)
+        _int32(offsets, "offsets", E + 1, logits)
+        _int32(rows, "rows", T * k, logits)
+        _int32(pos, "pos", T * k, logits)
+    _on_gpu(logits)
+    mxfp4_moe_route(logits, lt, logits.stride(0) if T > 1 else E, bias, T, E, k, _scores[score], renormalize, *out,
+                    stream=stream)
+    return out
+
+
+def _weights(t, T, k, like):
+    import torch
+    if t.dtype != torch.float32 or t.shape != (T, k) or not t.is_contiguous() or t.device != like.device:
+        raise ValueError("weights must be a contiguous f32 [%d, %d] tensor on %s" % (T, k, like.device))
+
+
+def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, stream=None):
+    """out[t] = residual[t] + sum_j weights[t, j] * y[pos[t, j]].
+
+    y [rows, N], bf16, f16 or f32, with contiguous rows; weights f32 [T, k]; pos
+    int32 [T, k] (row t * k + j without it; a place outside y adds nothing);
+    residual [T, N] of out's type, which may be out itself.  out's type is
+    out's, else out_dtype, else residual's, else bf16."""
+    import torch
+    if y.dim() != 2 or weights.dim() != 2:
+        raise ValueError("y must be [rows, N] and weights [T, k]")
+    R, N = y.shape
+    T, k = weights.shape
+    _rows_of(y, "y", R, N, y)
+    yt = _type(y)
+    _weights(weights, T, k, y)
+    if pos is not None:
+        _int32(pos, "pos", T * k, y)
+    elif R < T * k:
+        raise ValueError("y has %d rows, %d tokens of %d choices need %d" % (R, T, k, T * k))
+    if out is None:
+        dtype = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
+        out = torch.empty((T, N), dtype=dtype, device=y.device)
+    else:
+        _rows_of(out, "out", T, N, y)
+    if residual is not None:
+        _rows_of(residual, "residual", T, N, y)
+        if residual.dtype != out.dtype:
+            raise TypeError("residual is %s, out %s" % (residual.dtype, out.dtype))
+    _on_gpu(y)
+    mxfp4_moe_combine(y, yt, y.stride(0) if R > 1 else N, R, weights, pos, residual,
+                      residual.stride(0) if residual is not None and T > 1 else N, out, _type(out),
+                      out.stride(0) if T > 1 else N, T, k, N, stream=stream)
     return out

@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libmxfp4.so")
 PROBES_SOURCES = ["probes.hip", "probe_phases.hip", "probe_wide.hip"]
 PROBES_LIB = os.path.join(PKG, "libmxfp4_probes.so")
 SOURCES = ["mxfp4_api.hip", "quant_kernels.hip", "gemm_kernels.hip", "gemm_wide.hip", "experts_api.hip",
-           "gemv_kernels.hip"] + [
+           "gemv_kernels.hip", "route_kernels.hip", "combine_kernels.hip"] + [
     "gemm_table_%d.hip" % i for i in range(8)]
 ARCH = "gfx950"
 

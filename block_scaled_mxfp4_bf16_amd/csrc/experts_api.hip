@@ -26,9 +26,85 @@ inline bool matrix_fits(int64_t N, int64_t K) {
   return N <= (kMaxBytes - 1) / ((K + 1) / 2) && pad_to(N, 256) <= (kMaxBytes - 1) / pad_to(K / 32 + 1, 8);
 }
 
+// The caller's workspace if it gave one, else the library's, behind the
+// ticket words that the split-K products keep at zero.
+mxfp4_status_t take_workspace(void *given, size_t given_bytes, size_t need, hipStream_t stream, void **out) {
+  *out = given;
+  if (given) return given_bytes >= need && aligned(given, 256) ? MXFP4_OK : MXFP4_ERR_WORKSPACE;
+  if (need == 0) return MXFP4_OK;
+  void *p = nullptr;
+  const mxfp4_status_t st = get_workspace(kTicketBytes + need, stream, &p);
+  if (st == MXFP4_OK) *out = (char *)p + kTicketBytes;
+  return st;
+}
+
 }  // namespace
 
 extern "C" {
+
+mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream) {
+  if (bytes > ((size_t)1 << 46)) return MXFP4_ERR_UNSUPPORTED;
+  void *p = nullptr;
+  return get_workspace(bytes ? kTicketBytes + bytes : 0, (hipStream_t)stream, &p);
+}
+
+size_t mxfp4_moe_route_workspace_bytes(int64_t T, int64_t E) {
+  return T < 1 || E < 1 || T > kMaxRows || E > kRouteMaxExperts ? 0 : route_workspace_bytes(T, E);
+}
+
+mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const float *bias, int64_t T, int64_t E,
+                               int64_t k, int score, int renormalize, int32_t *ids, float *weights,
+                               int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace, size_t workspace_bytes,
+                               mxfp4_stream_t stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || ld < E || !known_type(x_type) || !offsets) return MXFP4_ERR_INVALID_ARG;
+  if (score != MXFP4_SCORE_SOFTMAX && score != MXFP4_SCORE_SIGMOID) return MXFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !ids || !weights || !rows || !pos)) return MXFP4_ERR_INVALID_ARG;
+  if (!aligned(logits, size_of(x_type)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4))
+    return MXFP4_ERR_INVALID_ARG;
+  if (T > kMaxRows || E > kRouteMaxExperts || k > kRouteMaxChoices || ld > ((int64_t)1 << 40))
+    return MXFP4_ERR_UNSUPPORTED;
+  void *ws = nullptr;
+  const mxfp4_status_t st =
+      take_workspace(workspace, workspace_bytes, route_workspace_bytes(T, E), (hipStream_t)stream, &ws);
+  if (st != MXFP4_OK) return st;
+  RouteArgs a{};
+  a.logits = logits;
+  a.x_type = x_type;
+  a.ld = ld;
+  a.bias = bias;
+  a.T = (int)T;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.score = score;
+  a.renorm = renormalize != 0;
+  a.ids = ids;
+  a.weights = weights;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.pos = pos;
+  a.hist = (int32_t *)ws;
+  return hip_status(launch_route(a, (hipStream_t)stream));
+}
+
+mxfp4_status_t mxfp4_moe_combine(const void *y, int y_type, int64_t ld_y, int64_t rows, const float *weights,
+                                 const int32_t *pos, const void *residual, int64_t ld_res, void *out, int out_type,
+                                 int64_t ld_out, int64_t T, int64_t k, int64_t N, mxfp4_stream_t stream) {
+  if (T < 0 || rows < 0 || N < 1 || k < 1 || !known_type(y_type) || !known_type(out_type)) return MXFP4_ERR_INVALID_ARG;
+  if (ld_y < N || ld_out < N || (residual && ld_res < N)) return MXFP4_ERR_INVALID_ARG;
+  if (T > 0 && (!weights || !out || (rows > 0 && !y))) return MXFP4_ERR_INVALID_ARG;
+  if (!aligned(y, size_of(y_type)) || !aligned(weights, 4) || !aligned(pos, 4) ||
+      !aligned(residual, size_of(out_type)) || !aligned(out, size_of(out_type)))
+    return MXFP4_ERR_INVALID_ARG;
+  const int64_t far = (int64_t)1 << 40;  // row counts and strides whose products stay below 2^63 bytes
+  if (N >= INT32_MAX - 4096 || k > kMaxRows || T > ((int64_t)1 << 20) * 64 || rows > ((int64_t)1 << 30) ||
+      ld_y > far / 1024 || ld_out > far / 1024 || (residual && ld_res > far / 1024))
+    return MXFP4_ERR_UNSUPPORTED;
+  if (T == 0) return MXFP4_OK;
+  CombineArgs a{y,        y_type, ld_y,     rows,   weights, pos, residual,
+                ld_res,   out,    out_type, ld_out, T,       N,   (int)k};
+  return hip_status(launch_combine(a, (hipStream_t)stream));
+}
 
 mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, const void *Bq_sh, const void *Bs_sh,
                           const int32_t *ids, int64_t experts, void *y, int y_type, int64_t ldy, int64_t M, int64_t N,

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/mxfp4.h"
+
 namespace mxfp4 {
 
 struct GemvArgs {
@@ -23,5 +25,42 @@ struct GemvArgs {
 };
 
 hipError_t launch_gemv(const GemvArgs &a, hipStream_t stream);
+
+// Largest number of experts and of choices of the router.
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxChoices = 32;
+
+struct RouteArgs {
+  const void *logits;
+  int x_type;
+  int64_t ld;
+  const float *bias;  // or null
+  int T, E, k, score, renorm;
+  int32_t *ids;
+  float *weights;
+  int32_t *offsets, *rows, *pos;
+  int32_t *hist;  // [blocks, E] counts, unless T is small
+  int blocks, per_block;
+};
+
+size_t route_workspace_bytes(int64_t T, int64_t E);
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+
+struct CombineArgs {
+  const void *y;
+  int y_type;
+  int64_t ld_y, rows;
+  const float *weights;
+  const int32_t *pos;    // or null: row t * k + j
+  const void *residual;  // or null; of the output's type
+  int64_t ld_res;
+  void *out;
+  int out_type;
+  int64_t ld_out;
+  int64_t T, N;
+  int k;
+};
+
+hipError_t launch_combine(const CombineArgs &a, hipStream_t stream);
 
 }  // namespace mxfp4

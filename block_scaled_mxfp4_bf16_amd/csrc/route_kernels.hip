@@ -1,0 +1,387 @@
+// The router of a mixture-of-experts block:
+//   g[t, e]   softmax over e, or sigmoid, of the logits
+//   ids[t]    the k experts of the largest g + bias, in falling order, ties to
+//             the lower expert; an expert whose logit or bias is -inf or NaN
+//             is never chosen (id -1, weight 0 once none is left)
+//   w[t, j]   g of the chosen, divided by their sum if asked
+// and the stable sort of the (token, choice) pairs by expert: offsets[e], the
+// pair at each sorted place (rows) and the place of each pair (pos).
+//
+// The choice is made on whole numbers: a value maps to an unsigned integer of
+// the same order, so the largest is a plain integer maximum.  Without a bias
+// the logits themselves order the experts (both scores rise with the logit);
+// with one, g + bias is formed in f64, since two f32 sums that round to the
+// same value would pick the wrong expert.  L lanes share a token, L = 16
+// wherever E <= 256 and k <= 16: a maximum over 16 lanes is four rotate steps
+// and serves four tokens of a wave at once.  The weights of the k chosen are
+// computed in f64, one lane each, and rounded once.
+#include <type_traits>
+
+#include "experts_device.hpp"
+#include "experts_internal.hpp"
+
+namespace mxfp4 {
+
+namespace {
+
+constexpr int kMaxExperts = kRouteMaxExperts;
+
+// The value of lane (l + N) % 16 of the lane's row of 16.
+template <int N>
+__device__ __forceinline__ uint32_t rotate16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 | N, 0xF, 0xF, false);
+}
+
+// All-reduce over groups of L lanes; `op` on u32, u64 or double values.
+template <int N, class T>
+__device__ __forceinline__ T rotated(T v) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, rotate16<N>(__builtin_bit_cast(uint32_t, v)));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t r = rotate16<N>((uint32_t)u) | ((uint64_t)rotate16<N>((uint32_t)(u >> 32)) << 32);
+    return __builtin_bit_cast(T, r);
+  }
+}
+template <int L, class T, class Op>
+__device__ __forceinline__ T all_reduce(T v, Op op) {
+  v = op(v, rotated<8>(v));
+  v = op(v, rotated<4>(v));
+  v = op(v, rotated<2>(v));
+  v = op(v, rotated<1>(v));
+  if constexpr (L >= 32) v = op(v, (T)__shfl_xor(v, 16));
+  if constexpr (L >= 64) v = op(v, (T)__shfl_xor(v, 32));
+  return v;
+}
+
+// Integers in the order of the values; 0 stands for "never chosen" and is
+// below every finite value's.  -0 counts as 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_of(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
+  return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+}
+
+// A logit as f32; +inf counts as the largest finite value, NaN as -inf.
+__device__ __forceinline__ float logit(const RouteArgs &a, int64_t row, int e) {
+  const int64_t at = row * a.ld + e;
+  float v;
+  if (a.x_type == MXFP4_TYPE_F32)
+    v = ((const float *)a.logits)[at];
+  else if (a.x_type == MXFP4_TYPE_BF16)
+    v = (float)((const __bf16 *)a.logits)[at];
+  else
+    v = (float)((const _Float16 *)a.logits)[at];
+  return v != v ? -__builtin_inff() : __builtin_fminf(v, 3.402823466e38f);
+}
+
+__device__ __forceinline__ bool lowest(float v) { return v == -__builtin_inff(); }
+
+enum { kPlain = 0, kSum = 1, kBias = 2 };
+
+// One token by the L lanes of the caller's group (V experts a lane, expert
+// l + L * v).  Lane j < k returns choice j.  kSum: the softmax's sum over all
+// experts is needed; kBias: g + bias orders them.
+template <int L, int V, int MODE>
+__device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l, int *id_out, float *w_out) {
+  using Key = typename std::conditional<MODE == kBias, uint64_t, uint32_t>::type;
+  const auto larger = [](auto p, auto q) { return p > q ? p : q; };
+  const auto smaller = [](int p, int q) { return p < q ? p : q; };
+  const auto plus = [](double p, double q) { return p + q; };
+  float x[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = l + L * v;
+    x[v] = e < a.E ? logit(a, t, e) : -__builtin_inff();
+  }
+  float top = 0.f;
+  double total = 1.0;
+  Key key[V];
+  if constexpr (MODE != kPlain) {
+    if (a.score == MXFP4_SCORE_SOFTMAX) {
+      float m = x[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) m = larger(m, x[v]);
+      top = all_reduce<L>(m, larger);
+      if (lowest(top)) top = 0.f;
+    }
+    double g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      g[v] = a.score == MXFP4_SCORE_SOFTMAX ? exp((double)x[v] - top) : 1.0 / (1.0 + exp(-(double)x[v]));
+    if (a.score == MXFP4_SCORE_SOFTMAX) {
+      double s = g[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) s += g[v];
+      total = all_reduce<L>(s, plus);
+    }
+    if constexpr (MODE == kBias) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = l + L * v;
+        const float b = e < a.E ? a.bias[e] : 0.f;
+        const double by = (a.score == MXFP4_SCORE_SOFTMAX ? g[v] / total : g[v]) + b;
+        key[v] = lowest(x[v]) || lowest(b) || b != b ? 0 : order_of(by);
+      }
+    }
+  }
+  if constexpr (MODE != kBias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = lowest(x[v]) ? 0 : order_of(x[v]);
+  }
+
+  int id = -1;
+  for (int j = 0; j < a.k; ++j) {
+    Key m = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = larger(m, key[v]);
+    m = all_reduce<L>(m, larger);
+    int c = INT32_MAX;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) c = key[v] == m ? l + L * v : c;
+    c = all_reduce<L>(c, smaller);
+    if (l == j) id = m ? c : -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = l + L * v == c ? 0 : key[v];
+    if constexpr (MODE == kPlain) {
+      if (j == 0 && a.score == MXFP4_SCORE_SOFTMAX) {  // the first choice is the largest logit
+        const uint32_t o = m;
+        top = m ? __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu)) : 0.f;
+      }
+    }
+  }
+
+  double w = 0.0;
+  if (id >= 0) {
+    const double xl = (double)logit(a, t, id);
+    w = a.score == MXFP4_SCORE_SOFTMAX ? exp(xl - top) / total : 1.0 / (1.0 + exp(-xl));
+  }
+  if (a.renorm) {
+    const double s = all_reduce<L>(w, plus);
+    w = s > 0.0 ? w / s : w;
+  }
+  *id_out = id;
+  *w_out = (float)w;
+}
+
+// Tokens [t0, t1) by the block's groups of L lanes: ids and weights, and the
+// count of each expert in `hist` (zeroed by the caller).
+template <int L, int V, int MODE, int THREADS>
+__device__ __forceinline__ void route_tokens(const RouteArgs &a, int64_t t0, int64_t t1, int *hist) {
+  const int l = threadIdx.x & (L - 1);
+  for (int64_t t = t0 + threadIdx.x / L; t < t1; t += THREADS / L) {
+    int id;
+    float w;
+    route_token<L, V, MODE>(a, t, l, &id, &w);
+    if (l < a.k) {
+      a.ids[t * a.k + l] = id;
+      a.weights[t * a.k + l] = w;
+      if (id >= 0) atomicAdd(&hist[id], 1);
+    }
+  }
+}
+
+// Exclusive sums of v[0 .. E), in place, by one wave.
+__device__ __forceinline__ int scan_experts(int *v, int E) {
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) >> 6;
+  const int lo = lane * per < E ? lane * per : E;
+  const int hi = lo + per < E ? lo + per : E;
+  int s = 0;
+  for (int e = lo; e < hi; ++e) s += v[e];
+  int incl = s;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  int run = incl - s;
+  for (int e = lo; e < hi; ++e) {
+    const int c = v[e];
+    v[e] = run;
+    run += c;
+  }
+  return __shfl(incl, 63);
+}
+
+// Sorted places of the pairs [p0, p1): each wave of the block takes a
+// contiguous run of them, counts its experts, and then walks its run 64 pairs
+// at a time; lanes of the same expert find each other by ballots over the
+// bits of the id.  next[e] is the first free place of expert e.
+template <int THREADS>
+__device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int64_t p1, const int *next,
+                                            int (*wave_next)[kMaxExperts]) {
+  constexpr int W = THREADS / 64;
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int64_t run = ((p1 - p0 + W - 1) / W + 63) / 64 * 64;
+  const int64_t lo = p0 + wave * run, hi = lo + run < p1 ? lo + run : p1;
+  for (int i = threadIdx.x; i < W * a.E; i += THREADS) wave_next[i / a.E][i % a.E] = 0;
+  __syncthreads();
+  for (int64_t p = lo + lane; p < hi; p += 64) {
+    const int id = a.ids[p];
+    if (id >= 0) atomicAdd(&wave_next[wave][id], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += THREADS) {
+    int at = next[e];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int c = wave_next[w][e];
+      wave_next[w][e] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(a.E);  // of every id below E
+  for (int64_t p = lo; p < hi; p += 64) {
+    const int64_t mine = p + lane;
+    const int id = mine < hi ? a.ids[mine] : -1;
+    uint64_t same = __ballot(id >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((id >> b) & 1);
+      same &= (id >> b) & 1 ? set : ~set;
+    }
+    const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
+    if (id >= 0) {
+      const int at = wave_next[wave][id] + before;
+      a.rows[at] = (int32_t)mine;
+      a.pos[mine] = at;
+    } else if (mine < hi) {
+      a.pos[mine] = -1;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0 && before == 0) wave_next[wave][id] += __builtin_popcountll(same);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+}  // namespace
+
+// First launch of many tokens: block b takes tokens [b * per_block, ...) and
+// leaves its expert counts in hist[b].
+template <int L, int V, int MODE>
+__global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a) {
+  __shared__ int hist[kMaxExperts];
+  for (int e = threadIdx.x; e < a.E; e += 256) hist[e] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * a.per_block;
+  route_tokens<L, V, MODE, 256>(a, t0, t0 + a.per_block < a.T ? t0 + a.per_block : a.T, hist);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += 256) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+}
+
+// Second launch: the same blocks add up the counts before theirs and place
+// their pairs.
+__global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a) {
+  __shared__ int next[kMaxExperts];    // all counts, then first place, of each expert
+  __shared__ int before[kMaxExperts];  // pairs of the expert in earlier blocks
+  __shared__ int wave_next[4][kMaxExperts];
+  __shared__ int used;
+  for (int e = threadIdx.x; e < a.E; e += 256) next[e] = before[e] = 0;
+  __syncthreads();
+  // `seg` threads share an expert's counts, each taking every seg-th block
+  int width = 1;
+  while (width < a.E && width < 256) width <<= 1;
+  const int seg = 256 / width;
+  for (int e = threadIdx.x & (width - 1); e < a.E; e += width) {
+    int all = 0, mine = 0;
+    for (int b = threadIdx.x / width; b < a.blocks; b += seg) {
+      const int c = a.hist[(int64_t)b * a.E + e];
+      all += c;
+      mine += b < (int)blockIdx.x ? c : 0;
+    }
+    atomicAdd(&next[e], all);
+    atomicAdd(&before[e], mine);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int n = scan_experts(next, a.E);
+    if (threadIdx.x == 0) used = n;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < a.E; e += 256) a.offsets[e] = next[e];
+    if (threadIdx.x == 0) a.offsets[a.E] = used;
+  }
+  const int64_t pairs = (int64_t)a.T * a.k;
+  for (int64_t p = used + (int64_t)blockIdx.x * 256 + threadIdx.x; p < pairs; p += (int64_t)a.blocks * 256)
+    a.rows[p] = -1;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += 256) next[e] += before[e];
+  const int64_t p0 = (int64_t)blockIdx.x * a.per_block * a.k;
+  const int64_t p1 = p0 + (int64_t)a.per_block * a.k;
+  place_pairs<256>(a, p0, p1 < pairs ? p1 : pairs, next, wave_next);
+}
+
+// Few tokens: all of it in one workgroup and one launch.
+template <int L, int V, int MODE>
+__global__ __launch_bounds__(512) void route_small_kernel(const RouteArgs a) {
+  __shared__ int next[kMaxExperts];
+  __shared__ int wave_next[8][kMaxExperts];
+  __shared__ int used;
+  for (int e = threadIdx.x; e < a.E; e += 512) next[e] = 0;
+  __syncthreads();
+  route_tokens<L, V, MODE, 512>(a, 0, a.T, next);
+  __syncthreads();  // the ids this block wrote are read back below
+  if (threadIdx.x < 64) {
+    const int n = scan_experts(next, a.E);
+    if (threadIdx.x == 0) used = n;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += 512) a.offsets[e] = next[e];
+  if (threadIdx.x == 0) a.offsets[a.E] = used;
+  const int pairs = a.T * a.k;
+  for (int p = used + threadIdx.x; p < pairs; p += 512) a.rows[p] = -1;
+  place_pairs<512>(a, 0, pairs, next, wave_next);
+}
+
+// Up to this many tokens one workgroup does everything.
+constexpr int kSmallTokens = 128;
+
+// Tokens per block otherwise: at most 256 blocks, whole passes of 16 tokens.
+static int64_t route_per_block(int64_t T) { return ((T + 255) / 256 + 15) / 16 * 16; }
+
+size_t route_workspace_bytes(int64_t T, int64_t E) {
+  if (T <= kSmallTokens) return 0;
+  const int64_t per = route_per_block(T);
+  return (size_t)((T + per - 1) / per * E * 4);
+}
+
+template <int L, int V, int MODE>
+static hipError_t run_route(RouteArgs a, hipStream_t stream) {
+  if (a.T <= kSmallTokens) {
+    route_small_kernel<L, V, MODE><<<1, 512, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  a.per_block = (int)route_per_block(a.T);
+  a.blocks = (a.T + a.per_block - 1) / a.per_block;
+  route_choose_kernel<L, V, MODE><<<a.blocks, 256, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  route_place_kernel<<<a.blocks, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int MODE>
+static hipError_t run_route_mode(const RouteArgs &a, hipStream_t stream) {
+  if (a.k <= 16) {
+    if (a.E <= 64) return run_route<16, 4, MODE>(a, stream);
+    if (a.E <= 128) return run_route<16, 8, MODE>(a, stream);
+    if (a.E <= 256) return run_route<16, 16, MODE>(a, stream);
+  } else if (a.E <= 256) {
+    return run_route<32, 8, MODE>(a, stream);
+  }
+  return run_route<64, 16, MODE>(a, stream);
+}
+
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
+  if (a.bias) return run_route_mode<kBias>(a, stream);
+  if (a.score == MXFP4_SCORE_SOFTMAX && !a.renorm) return run_route_mode<kSum>(a, stream);
+  return run_route_mode<kPlain>(a, stream);
+}
+
+}  // namespace mxfp4

@@ -318,6 +318,64 @@ MXFP4_API mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, cons
                                     const int32_t *ids, int64_t experts, void *y, int y_type, int64_t ldy, int64_t M,
                                     int64_t N, int64_t K, int64_t repeat, int gated, mxfp4_stream_t stream);
 
+/* Device memory of the routing and the grouped product.  Each of them takes */
+/* `workspace`, 256-byte aligned and of at least the stated bytes; its        */
+/* contents need no clearing and are lost, and calls that share it must not  */
+/* overlap in time.  NULL: the library's own workspace of (device, stream),  */
+/* as mxfp4_gemm has it: created or grown by the first call that needs more, */
+/* or ahead of time by mxfp4_reserve_bytes (before graph capture, say).      */
+MXFP4_API mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream);
+
+/* The router: which experts each token takes, with which weights, and the   */
+/* (token, choice) pairs sorted by expert.                                   */
+/*   g[t, e] = softmax over e, or sigmoid, of logits[t, e]                    */
+/*   ids[t, 0..k) = the experts of the largest logits (bias == NULL) or of   */
+/*       the largest g + bias, in falling order, equal ones by number        */
+/*   weights[t, j] = g[t, ids[t, j]], divided by the sum over j if           */
+/*       renormalize != 0 and that sum is not zero                           */
+/* An expert whose logit or bias is -inf or NaN is never chosen; a token     */
+/* with fewer than k others has id -1 and weight 0 in the places left over.  */
+/* +inf counts as the largest finite logit.  Equal values are equal as the   */
+/* input's type holds them; g + bias is formed in f64, weights are computed  */
+/* in f64 and rounded once.                                                  */
+/*   logits  [T, E] of x_type, rows ld elements apart               (input)  */
+/*   bias    f32 [E] or NULL                                         (input)  */
+/*   ids     int32 [T, k];  weights  f32 [T, k]                     (output) */
+/*   offsets int32 [E + 1]: pairs of expert e lie at offsets[e] ..            */
+/*           offsets[e + 1] - 1 of the sorted order                 (output) */
+/*   rows    int32 [T * k]: the pair t * k + j at each sorted place, pairs   */
+/*           of one expert in rising order; -1 past offsets[E]       (output) */
+/*   pos     int32 [T, k]: the sorted place of each pair; -1 for id -1        */
+/* T may be 0.  The result is the same every time.                            */
+/* Errors: INVALID_ARG (null, T < 0, E < 1, k < 1, k > E, ld < E, unknown     */
+/*         type or score, a pointer not aligned to its type);                */
+/*         UNSUPPORTED (E > 1024, k > 32, T > 2^20); WORKSPACE; HIP.          */
+typedef enum { MXFP4_SCORE_SOFTMAX = 0, MXFP4_SCORE_SIGMOID = 1 } mxfp4_score_t;
+MXFP4_API size_t mxfp4_moe_route_workspace_bytes(int64_t T, int64_t E);
+MXFP4_API mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const float *bias, int64_t T,
+                                         int64_t E, int64_t k, int score, int renormalize, int32_t *ids,
+                                         float *weights, int32_t *offsets, int32_t *rows, int32_t *pos,
+                                         void *workspace, size_t workspace_bytes, mxfp4_stream_t stream);
+
+/* The weighted sum of each token's expert rows:                             */
+/*   out[t, n] = residual[t, n] + sum_j weights[t, j] * y[pos[t, j], n]       */
+/* in f32, choices in order, the residual last, rounded once to out's type.  */
+/*   y        [rows, N] of y_type, ld_y elements apart              (input)  */
+/*   weights  f32 [T, k]                                             (input)  */
+/*   pos      int32 [T, k]: the row of y of each choice; one outside         */
+/*            [0, rows) adds nothing.  NULL: row t * k + j           (input)  */
+/*   residual [T, N] of out's type, ld_res elements apart, or NULL; may be   */
+/*            out itself                                             (input)  */
+/*   out      [T, N] of out_type, ld_out elements apart             (output) */
+/* T may be 0 (and rows, which then, or with rows 0, may have a null y).     */
+/* Errors: INVALID_ARG (null, T or rows < 0, N < 1, k < 1, a row stride < N,  */
+/*         unknown type, a pointer not aligned to its type);                 */
+/*         UNSUPPORTED (N >= 2^31 - 4096, k > 2^20).                          */
+MXFP4_API mxfp4_status_t mxfp4_moe_combine(const void *y, int y_type, int64_t ld_y, int64_t rows,
+                                           const float *weights, const int32_t *pos, const void *residual,
+                                           int64_t ld_res, void *out, int out_type, int64_t ld_out, int64_t T,
+                                           int64_t k, int64_t N, mxfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
