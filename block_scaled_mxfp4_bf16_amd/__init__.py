@@ -65,6 +65,8 @@ def _load():
         "mxfp4_reserve_bytes": (I, [SZ, P]),
         "mxfp4_moe_route_workspace_bytes": (SZ, [I64, I64]),
         "mxfp4_moe_route": (I, [P, I, I64, P, I64, I64, I64, I, I, P, P, P, P, P, P, SZ, P]),
+        "mxfp4_gemm_grouped_workspace_bytes": (SZ, [I64, I64, I64]),
+        "mxfp4_gemm_grouped": (I, [P, I64, I64, P, P, I64, P, P, I64, P, I64, I64, I64, I64, I, P, SZ, P]),
         "mxfp4_moe_combine": (I, [P, I, I64, I64, P, P, P, I64, P, I, I64, I64, I64, I64, P]),
     }
     for name, (res, args) in sigs.items():
@@ -86,7 +88,7 @@ def exported_symbols():
             "mxfp4_gemm_ex", "mxfp4_gemm_noalloc", "mxfp4_gemm_q", "mxfp4_gemm_q_schedule_name", "mxfp4_reserve", "mxfp4_status_string", "mxfp4_last_hip_error", "mxfp4_gemm_schedule_name",
             "mxfp4_set_quant_mode", "mxfp4_set_schedule_override", "mxfp4_list_schedules",
             "mxfp4_gemv", "mxfp4_reserve_bytes", "mxfp4_moe_route_workspace_bytes", "mxfp4_moe_route",
-            "mxfp4_moe_combine"]
+            "mxfp4_gemm_grouped_workspace_bytes", "mxfp4_gemm_grouped", "mxfp4_moe_combine"]
 
 
 def _check(rc: int, what: str):
@@ -222,6 +224,18 @@ def mxfp4_moe_route(logits, x_type: int, ld: int, bias, T: int, E: int, k: int, 
     _check(_load().mxfp4_moe_route(_ptr(logits), x_type, ld, _ptr(bias), T, E, k, score, int(bool(renormalize)),
                                    _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(rows), _ptr(pos), _ptr(workspace),
                                    workspace_bytes, _stream(stream)), "mxfp4_moe_route")
+
+
+def mxfp4_gemm_grouped_workspace_bytes(R: int, K: int, experts: int) -> int:
+    return _load().mxfp4_gemm_grouped_workspace_bytes(R, K, experts)
+
+
+def mxfp4_gemm_grouped(A, lda: int, a_rows: int, Bq_sh, Bs_sh, experts: int, offsets, rows, repeat: int, C, ldc: int,
+                       R: int, N: int, K: int, gated: bool = False, workspace=None, workspace_bytes: int = 0,
+                       stream=None):
+    _check(_load().mxfp4_gemm_grouped(_ptr(A), lda, a_rows, _ptr(Bq_sh), _ptr(Bs_sh), experts, _ptr(offsets),
+                                      _ptr(rows), repeat, _ptr(C), ldc, R, N, K, int(bool(gated)), _ptr(workspace),
+                                      workspace_bytes, _stream(stream)), "mxfp4_gemm_grouped")
 
 
 def mxfp4_moe_combine(y, y_type: int, ld_y: int, rows: int, weights, pos, residual, ld_res: int, out, out_type: int,
@@ -381,6 +395,40 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
         return out
     mxfp4_gemv(x, xt, x.stride(0) if x.shape[0] > 1 else K, Bw, Bs, ids, E, out, _type(out),
                out.stride(0) if M > 1 else cols, M, N, K, repeat, gated, stream)
+    return out
+
+
+def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: bool = False, out=None, stream=None):
+    """C[p] = Q(A[row(p)]) * B_e^T for offsets[e] <= p < offsets[e + 1], bf16.
+
+    A [a_rows, K] bf16 with contiguous rows; Bw, Bs E matrices from
+    prepare_experts; offsets int32 [E + 1].  row(p) is rows[p] // repeat (int32
+    [R], from moe_route with repeat = k), or p without rows.  gated: N/2
+    columns, silu(first half) * second.  Rows of no group are zero."""
+    import torch
+    if A.dim() != 2:
+        raise ValueError("A must be [rows, K]")
+    T, K = A.shape
+    _rows_of(A, "A", T, K, A)
+    if A.dtype != torch.bfloat16:
+        raise TypeError("A must be bf16, not %s" % A.dtype)
+    E = _prepared(Bw, Bs, N, K, A)
+    _int32(offsets, "offsets", E + 1, A)
+    if rows is not None:
+        _int32(rows, "rows", rows.numel(), A)
+        R = rows.numel()
+    else:
+        R = T
+    cols = N // 2 if gated else N
+    if out is None:
+        out = torch.empty((R, cols), dtype=torch.bfloat16, device=A.device)
+    else:
+        _rows_of(out, "out", R, cols, A)
+        if out.dtype != torch.bfloat16:
+            raise TypeError("out must be bf16, not %s" % out.dtype)
+    _on_gpu(A)
+    mxfp4_gemm_grouped(A, A.stride(0) if T > 1 else K, T, Bw, Bs, E, offsets, rows, repeat, out,
+                       out.stride(0) if R > 1 else cols, R, N, K, gated, stream=stream)
     return out
 
 

@@ -16,7 +16,8 @@ LIB = os.path.join(PKG, "libmxfp4.so")
 PROBES_SOURCES = ["probes.hip", "probe_phases.hip", "probe_wide.hip"]
 PROBES_LIB = os.path.join(PKG, "libmxfp4_probes.so")
 SOURCES = ["mxfp4_api.hip", "quant_kernels.hip", "gemm_kernels.hip", "gemm_wide.hip", "experts_api.hip",
-           "gemv_kernels.hip", "route_kernels.hip", "combine_kernels.hip"] + [
+           "gemv_kernels.hip", "route_kernels.hip", "combine_kernels.hip",
+           "grouped_kernels.hip"] + [
     "gemm_table_%d.hip" % i for i in range(8)]
 ARCH = "gfx950"
 
@@ -39,7 +40,7 @@ HIPCC_FLAGS = [
 # AGPRs, so long accumulation loops get copies between every pair of
 # instructions; keeping accumulators in VGPRs lets them update in place.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-EXTRA_FLAGS = {"gemm_wide.hip": VGPR_FORM, "gemv_kernels.hip": VGPR_FORM, "probes.hip": VGPR_FORM, "probe_wide.hip": VGPR_FORM}
+EXTRA_FLAGS = {"gemm_wide.hip": VGPR_FORM, "gemv_kernels.hip": VGPR_FORM, "grouped_kernels.hip": VGPR_FORM, "probes.hip": VGPR_FORM, "probe_wide.hip": VGPR_FORM}
 
 
 def hipcc() -> str:

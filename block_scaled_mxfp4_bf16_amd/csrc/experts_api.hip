@@ -10,6 +10,7 @@ namespace {
 
 const int64_t kMaxBytes = (int64_t)1 << 31;  // 32-bit offsets inside the kernels
 const int64_t kMaxRows = (int64_t)1 << 20;
+const int64_t kMaxGroups = 4096;
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -85,6 +86,51 @@ mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const
   a.pos = pos;
   a.hist = (int32_t *)ws;
   return hip_status(launch_route(a, (hipStream_t)stream));
+}
+
+size_t mxfp4_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int64_t experts) {
+  if (R < 1 || K < 1 || experts < 1 || R > kMaxRows || K >= kMaxBytes || experts > kMaxGroups) return 0;
+  return grouped_workspace_bytes(R, K, experts);
+}
+
+mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, const void *Bq_sh, const void *Bs_sh,
+                                  int64_t experts, const int32_t *offsets, const int32_t *rows, int64_t repeat,
+                                  void *C, int64_t ldc, int64_t R, int64_t N, int64_t K, int gated, void *workspace,
+                                  size_t workspace_bytes, mxfp4_stream_t stream) {
+  if (R < 0 || a_rows < 0 || N < 1 || K < 1 || experts < 1 || repeat < 1) return MXFP4_ERR_INVALID_ARG;
+  if (!Bq_sh || !Bs_sh || !offsets || (R > 0 && !C) || (a_rows > 0 && !A)) return MXFP4_ERR_INVALID_ARG;
+  if (lda < K || ldc < (gated ? N / 2 : N)) return MXFP4_ERR_INVALID_ARG;
+  if (K % 32 != 0 || N % 16 != 0 || (gated && N % 32 != 0)) return MXFP4_ERR_UNSUPPORTED;
+  if (R > kMaxRows || a_rows > kMaxRows || experts > kMaxGroups || repeat > INT32_MAX || !matrix_fits(N, K) ||
+      lda > ((int64_t)1 << 30) || ldc > ((int64_t)1 << 30))
+    return MXFP4_ERR_UNSUPPORTED;
+  if (!aligned(A, 16) || lda % 8 != 0 || !aligned(Bq_sh, 16) || !aligned(Bs_sh, 16) || !aligned(offsets, 4) ||
+      !aligned(rows, 4) || !aligned(C, 2))
+    return MXFP4_ERR_INVALID_ARG;
+  if (R == 0) return MXFP4_OK;
+  void *ws = nullptr;
+  const mxfp4_status_t st = take_workspace(workspace, workspace_bytes, grouped_workspace_bytes(R, K, experts),
+                                           (hipStream_t)stream, &ws);
+  if (st != MXFP4_OK) return st;
+  GroupedArgs a{};
+  a.A = (const uint16_t *)A;
+  a.lda = lda;
+  a.a_rows = a_rows;
+  a.Bw = (const uint8_t *)Bq_sh;
+  a.Bs = (const uint8_t *)Bs_sh;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.C = (uint16_t *)C;
+  a.ldc = ldc;
+  a.R = (int)R;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.E = (int)experts;
+  a.repeat = (int)repeat;
+  a.gated = gated != 0;
+  a.sw = sw_quant();
+  a.ws = (uint8_t *)ws;
+  return hip_status(launch_grouped(a, (hipStream_t)stream));
 }
 
 mxfp4_status_t mxfp4_moe_combine(const void *y, int y_type, int64_t ld_y, int64_t rows, const float *weights,

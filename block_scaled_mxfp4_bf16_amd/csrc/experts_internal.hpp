@@ -46,6 +46,23 @@ struct RouteArgs {
 size_t route_workspace_bytes(int64_t T, int64_t E);
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 
+struct GroupedArgs {
+  const uint16_t *A;
+  int64_t lda, a_rows;
+  const uint8_t *Bw, *Bs;
+  const int32_t *offsets;
+  const int32_t *rows;  // or null: output row p takes row p of A
+  uint16_t *C;
+  int64_t ldc;
+  int R, N, K, E, repeat, gated, sw;
+  uint8_t *ws;
+  uint8_t *codes, *scales;  // in ws, `quads` blocks of 64 rows each
+  int quads;
+};
+
+size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E);
+hipError_t launch_grouped(GroupedArgs a, hipStream_t stream);
+
 struct CombineArgs {
   const void *y;
   int y_type;

@@ -1,0 +1,264 @@
+// The MXFP4 product of ragged row groups, one weight matrix per group:
+//   C[p] = Q(A[row(p)]) * B_e^T   for offsets[e] <= p < offsets[e + 1]
+// with row(p) = rows[p] / repeat, or p without `rows`; and its gated form.
+//
+// Two launches.  The first gathers the rows of each group, quantizes them and
+// writes them in the layout that the matrix instruction takes, so that the
+// second reads every operand as whole 1 KiB blocks.  The group sizes stay on
+// the device: each workgroup finds its rows from the offsets by a scan over
+// the experts, and the grids are sized for the worst case.
+#include "experts_internal.hpp"
+#include "grouped_device.hpp"
+#include "mxfp4_internal.hpp"
+
+namespace mxfp4 {
+
+// Quads that R rows in E groups can take at most: every group wastes less
+// than one, and no more groups have rows than there are rows.
+static int64_t grouped_quads(int64_t R, int64_t E) { return (R + 63 * (E < R ? E : R)) / 64; }
+
+static int64_t k_steps(int64_t K) { return (K + 127) / 128; }
+
+size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E) {
+  return (size_t)grouped_quads(R, E) * (size_t)k_steps(K) * (4096 + 256);
+}
+
+// Gather and quantize.  One wave takes one K step of a quad, four waves the
+// steps of a workgroup.  Four lanes share a group of 32 elements (as in the
+// large-M product's quantizer), so a load covers 16 rows of 64 bytes; all 16
+// loads of a wave are issued before the first is used.  Rows past the group
+// and groups past K load as zeros and become zero codes with scale byte 0.
+__global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int KS = (a.K + 127) >> 7;
+  const UnitFinder<64> finder(a.offsets, a.E, a.R, lane);
+
+  // output rows of no group are zero
+  if (blockIdx.y == 0) {
+    int lo, hi, unused;
+    group_range(a.offsets, 0, a.R, lo, unused);
+    group_range(a.offsets, a.E - 1, a.R, unused, hi);
+    const int cols = a.gated ? a.N >> 1 : a.N;
+    const int outside = lo + (a.R - hi);
+    for (int i = blockIdx.x; i < outside; i += gridDim.x) {
+      uint16_t *c = a.C + (int64_t)(i < lo ? i : hi + i - lo) * a.ldc;
+      for (int n = threadIdx.x; n < cols; n += 256) c[n] = 0;
+    }
+  }
+
+  const int quad = blockIdx.x;
+  if (quad >= finder.total) return;
+  const Unit u = finder.find(quad);
+  const int ks = blockIdx.y * 4 + wave;
+  if (u.expert < 0 || ks >= KS) return;
+
+  u32x4 w[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 16 * j + (lane >> 2);
+    int64_t src = -1;
+    if (r < u.rows) {
+      const int p = u.row + r;
+      src = a.rows ? (a.rows[p] < 0 ? -1 : a.rows[p] / a.repeat) : p;
+    }
+    const bool ok = src >= 0 && src < a.a_rows;
+    const uint16_t *row = a.A + (ok ? src : 0) * a.lda;
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      const int k = ks * 128 + ch * 32 + (lane & 3) * 8;
+      w[j][ch] = u32x4{0, 0, 0, 0};
+      if (ok && k < a.K) w[j][ch] = *(const u32x4 *)(row + k);
+    }
+  }
+  const int live = (u.rows + 15) >> 4;  // tiles with a row
+  uint32_t *codes = (uint32_t *)(a.codes + ((int64_t)u.tile * KS + ks) * 1024);
+  uint32_t dw[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j < live) {
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t s;
+        // lane = 4 * row + quarter: dword (16 * ch + row) * 4 + quarter of the block
+        codes[(int64_t)j * KS * 256 + ch * 64 + lane] = quant_quarter(w[j][ch], a.sw, &s);
+        dw[ch] |= s << (8 * j);
+      }
+    }
+  }
+  // lane 4 * row + c writes the scales of operand lane 16 * c + row
+  const int c = lane & 3;
+  const uint32_t d = c == 0 ? dw[0] : (c == 1 ? dw[1] : (c == 2 ? dw[2] : dw[3]));
+  ((uint32_t *)(a.scales + ((int64_t)(u.tile >> 2) * KS + ks) * 256))[c * 16 + (lane >> 2)] = d;
+}
+
+__device__ __forceinline__ v4f mfma_fp4(const u32x4 &a, const u32x4 &b, const v4f &c, uint32_t sa, uint32_t sb) {
+  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// Workgroup: 16 * MT rows of one group x 16 * NT columns, all of K; wave w
+// takes steps w, w + WK, ... with D steps in flight.  With `gated` the first
+// NT / 2 subtiles are gate columns and the others their up columns.
+template <int MT, int NT, int WK, int D>
+__global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedArgs a, int n_tiles) {
+  __shared__ __attribute__((aligned(16))) float red[WK * MT * NT * 256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q4 = lane >> 4;
+  const UnitFinder<16 * MT> finder(a.offsets, a.E, a.R, lane);
+  const int64_t work = (int64_t)finder.total * n_tiles;
+  for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
+    const int index = (int)(item / n_tiles);
+    const int n_tile = (int)(item - (int64_t)index * n_tiles);
+    const Unit u = finder.find(index);
+    // only offsets that are no offsets lead past the packed rows
+    if (u.expert < 0 || (u.tile >> 2) + (MT + 3) / 4 > a.quads) return;
+
+    const int N = a.N, K = a.K;
+    const int KS = (K + 127) >> 7;
+    const int gp = ((K >> 5) + 7) & ~7;
+    const int b_bytes = (N >> 4) * K * 8;
+    const int s_bytes = ((N + 255) >> 8) * 8 * gp * 32;
+    const int rows = u.rows < 16 * MT ? u.rows : 16 * MT;
+    const int tiles = (rows + 15) >> 4;
+    const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(a.codes + (int64_t)u.tile * KS * 1024), 0, tiles * KS * 1024, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t as_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(a.scales + (int64_t)(u.tile >> 2) * KS * 256), 0, ((MT + 3) / 4) * KS * 256, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t b_rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(a.Bw + (int64_t)u.expert * b_bytes), 0, b_bytes, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t s_rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(a.Bs + (int64_t)u.expert * s_bytes), 0, s_bytes, kRsrcWord3);
+
+    const int groups = N >> 4;
+    const int cols = a.gated ? 8 * NT : 16 * NT;
+    const int first = n_tile * (cols >> 4);
+    int gw[NT];
+    bool gok[NT];
+  #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (a.gated) {
+        const int c = first + (nt % (NT / 2));
+        gok[nt] = c < (groups >> 1);
+        gw[nt] = nt < NT / 2 ? c : (groups >> 1) + c;
+      } else {
+        gw[nt] = first + nt;
+        gok[nt] = gw[nt] < groups;
+      }
+    }
+    const int tile_shift = 8 * (u.tile & 3);  // of the first tile's byte in a scale dword (0 unless MT < 4)
+
+    struct Stage {
+      u32x4 x[MT];
+      uint32_t xs[(MT + 3) / 4];
+      u32x4 b[NT];
+      uint32_t s[NT];
+    };
+    auto load = [&](int ks, Stage &st) {
+      const bool ok = ks < KS;
+      // a K chunk past the end meets zero rows of A; it is left out of range
+      // only where it would run past the matrix
+      const bool bk = ok && (4 * ks + q4) * 32 < K;
+  #pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        st.b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
+            b_rsrc, off_or_oob(bk && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
+        st.s[nt] = __builtin_amdgcn_raw_buffer_load_b32(
+            s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
+      }
+  #pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        st.x[mt] = __builtin_amdgcn_raw_buffer_load_b128(
+            a_rsrc, off_or_oob(ok && mt < tiles, (mt * KS + ks) * 1024 + lane * 16), 0, 0);
+  #pragma unroll
+      for (int q = 0; q < (MT + 3) / 4; ++q)
+        st.xs[q] = __builtin_amdgcn_raw_buffer_load_b32(as_rsrc, off_or_oob(ok, (q * KS + ks) * 256 + lane * 4), 0, 0);
+    };
+
+    v4f acc[MT][NT];
+  #pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+  #pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](int ks, const Stage &st) {
+  #pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t sb = (st.s[nt] >> (8 * ((gw[nt] & 1) + 2 * (ks & 1)))) & 0xFFu;
+  #pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t sa = (st.xs[mt >> 2] >> (tile_shift + 8 * (mt & 3))) & 0xFFu;
+          acc[mt][nt] = mfma_fp4(st.x[mt], st.b[nt], acc[mt][nt], sa, sb);
+        }
+      }
+    };
+
+    Stage st[D];
+  #pragma unroll
+    for (int d = 0; d < D; ++d) load(wave + WK * d, st[d]);
+    const int rounds = (KS + WK * D - 1) / (WK * D);
+    for (int it = 0; it < rounds; ++it) {
+  #pragma unroll
+      for (int d = 0; d < D; ++d) {
+        compute(wave + WK * (it * D + d), st[d]);
+        load(wave + WK * ((it + 1) * D + d), st[d]);
+      }
+    }
+
+  #pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+  #pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+        for (int r = 0; r < 4; ++r) red[((wave * MT + mt) * NT + nt) * 256 + r * 64 + lane] = acc[mt][nt][r];
+    __syncthreads();
+    auto sum = [&](int row, int nt, int n) {
+      const int at = ((row >> 4) * NT + nt) * 256 + (row & 3) * 64 + ((row >> 2) & 3) * 16 + n;
+      float v = 0.f;
+  #pragma unroll
+      for (int w = 0; w < WK; ++w) v += red[w * MT * NT * 256 + at];
+      return v;
+    };
+    const int out_cols = a.gated ? N >> 1 : N;
+    for (int j = threadIdx.x; j < rows * cols; j += 64 * WK) {
+      const int row = j / cols, c = j - row * cols;
+      const int col = n_tile * cols + c;
+      if (col >= out_cols) continue;
+      float v = sum(row, c >> 4, c & 15);
+      if (a.gated) v = gated_silu(v, sum(row, NT / 2 + (c >> 4), c & 15));
+      ((__bf16 *)a.C)[(int64_t)(u.row + row) * a.ldc + col] = (__bf16)v;
+    }
+    __syncthreads();  // before the next item's sums
+  }
+}
+
+// Workgroups of a launch (threads of a grid dimension are limited to 2^32).
+constexpr int64_t kMaxGrid = 1 << 22;
+
+template <int MT, int NT, int WK, int D>
+static hipError_t run_stream(const GroupedArgs &a, hipStream_t stream) {
+  const int cols = a.gated ? 8 * NT : 16 * NT;
+  const int out_cols = a.gated ? a.N >> 1 : a.N;
+  const int n_tiles = (out_cols + cols - 1) / cols;
+  const int64_t units = ((int64_t)a.R + (int64_t)(16 * MT - 1) * (a.E < a.R ? a.E : a.R)) / (16 * MT);
+  const int64_t items = units * n_tiles;
+  grouped_stream_kernel<MT, NT, WK, D>
+      <<<(unsigned)(items < kMaxGrid ? items : kMaxGrid), 64 * WK, 0, stream>>>(a, n_tiles);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped(GroupedArgs a, hipStream_t stream) {
+  const int64_t quads = grouped_quads(a.R, a.E), KS = k_steps(a.K);
+  a.quads = (int)quads;
+  a.codes = a.ws;
+  a.scales = a.ws + quads * KS * 4096;
+  pack_rows_kernel<<<dim3((unsigned)quads, (unsigned)((KS + 3) / 4)), 256, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t mean = a.R / (a.E < a.R ? a.E : a.R);  // rows of a group, were they even
+  if (mean <= 16) return run_stream<1, 2, 8, 2>(a, stream);
+  return run_stream<4, 4, 4, 2>(a, stream);
+}
+
+}  // namespace mxfp4

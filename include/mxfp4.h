@@ -357,6 +357,36 @@ MXFP4_API mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t
                                          float *weights, int32_t *offsets, int32_t *rows, int32_t *pos,
                                          void *workspace, size_t workspace_bytes, mxfp4_stream_t stream);
 
+/* The MXFP4 product of ragged row groups, one prepared matrix per group:    */
+/*   C[p, n] = sum_k Q(A[row(p)])[k] * B_e[n, k]                              */
+/*             for offsets[e] <= p < offsets[e + 1]                           */
+/* with row(p) = rows[p] / repeat, or p where rows is NULL, and Q the         */
+/* quantization of mxfp4_quantize; and its gated form.  With the offsets and  */
+/* rows of mxfp4_moe_route and repeat = k it takes each token's row to the   */
+/* experts it chose.  f32 sums in a fixed order, rounded once.  The group    */
+/* sizes stay on the device; the host waits for nothing.                     */
+/*   A        [a_rows, K] bf16, rows lda elements apart             (input)  */
+/*   Bq_sh, Bs_sh  `experts` prepared matrices                       (input)  */
+/*   offsets  int32 [experts + 1], rising, within [0, R]             (input)  */
+/*   rows     int32 [R] or NULL; a row(p) outside [0, a_rows) counts as a    */
+/*            row of zeros                                           (input)  */
+/*   C        [R, N] (gated: [R, N / 2]) bf16, rows ldc elements apart;       */
+/*            rows of no group are set to zero                      (output) */
+/* R may be 0.  A must be finite; offsets that do not rise or leave [0, R]   */
+/* give rows without meaning, but nothing outside the buffers is touched.    */
+/* Errors: INVALID_ARG (null, R or a_rows < 0, N, K, experts or repeat < 1,   */
+/*         lda < K, ldc < C's columns, A or its row stride not 16-byte        */
+/*         aligned, B not 16-byte aligned, C not 2-byte aligned);             */
+/*         UNSUPPORTED (K % 32 != 0, N % 16 != 0, gated with N % 32 != 0, a  */
+/*         matrix beyond 2^31 bytes, R or a_rows > 2^20, experts > 4096);      */
+/*         WORKSPACE; HIP.                                                    */
+MXFP4_API size_t mxfp4_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int64_t experts);
+MXFP4_API mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, const void *Bq_sh,
+                                            const void *Bs_sh, int64_t experts, const int32_t *offsets,
+                                            const int32_t *rows, int64_t repeat, void *C, int64_t ldc, int64_t R,
+                                            int64_t N, int64_t K, int gated, void *workspace, size_t workspace_bytes,
+                                            mxfp4_stream_t stream);
+
 /* The weighted sum of each token's expert rows:                             */
 /*   out[t, n] = residual[t, n] + sum_j weights[t, j] * y[pos[t, j], n]       */
 /* in f32, choices in order, the residual last, rounded once to out's type.  */
