@@ -102,7 +102,7 @@ mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, co
   if (lda < K || ldc < (gated ? N / 2 : N)) return MXFP4_ERR_INVALID_ARG;
   if (K % 32 != 0 || N % 16 != 0 || (gated && N % 32 != 0)) return MXFP4_ERR_UNSUPPORTED;
   if (R > kMaxRows || a_rows > kMaxRows || experts > kMaxGroups || repeat > INT32_MAX || !matrix_fits(N, K) ||
-      lda > ((int64_t)1 << 30) || ldc > ((int64_t)1 << 30))
+      N > kMaxRows || lda > ((int64_t)1 << 30) || ldc > ((int64_t)1 << 22))
     return MXFP4_ERR_UNSUPPORTED;
   if (!aligned(A, 16) || lda % 8 != 0 || !aligned(Bq_sh, 16) || !aligned(Bs_sh, 16) || !aligned(offsets, 4) ||
       !aligned(rows, 4) || !aligned(C, 2))

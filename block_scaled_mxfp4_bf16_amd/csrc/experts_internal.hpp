@@ -56,8 +56,10 @@ struct GroupedArgs {
   int64_t ldc;
   int R, N, K, E, repeat, gated, sw;
   uint8_t *ws;
-  uint8_t *codes, *scales;  // in ws, `quads` blocks of 64 rows each
-  int quads;
+  // set by launch_grouped: in ws, the list of units and the packed rows
+  int4 *plan;
+  uint8_t *codes, *scales;
+  int quads, max_units, unit_rows, unit_shift;
 };
 
 size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E);

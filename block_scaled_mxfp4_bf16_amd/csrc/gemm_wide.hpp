@@ -84,13 +84,6 @@ __device__ __forceinline__ v4f mfma_fp4_sel(const v8i &a, const v8i &b, const v4
   }
 }
 
-// Uniform part of a buffer offset, moved out of range (bit 31) unless
-// `in_range`; the lane's part is added to it afterwards (all offsets stay
-// below 2^31, so the sum is out of range exactly when the flag is set).
-__device__ __forceinline__ int uniform_off(bool in_range, int off) {
-  return off | (in_range ? 0 : (int)0x80000000u);
-}
-
 // Workgroup: W waves (two per SIMD when W = 8), output tile of 16*MW rows x
 // 16*NW columns, K steps [S0, S1) of its split; wave w takes steps S0 + w,
 // S0 + w + W, ...  Each wave keeps the whole tile's accumulators in
@@ -99,14 +92,6 @@ __device__ __forceinline__ int uniform_off(bool in_range, int off) {
 // slots (one step's NW operand blocks each) instead of registers, so the
 // registers that would have held them hold deeper A stages; each lane reads
 // back exactly the 16 bytes it loaded, right before the step's MFMAs.
-// s_waitcnt for vmcnt <= N, expcnt and lgkmcnt left alone (gfx9 encoding:
-// vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8).
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N <= 63, "vmcnt is six bits");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
 // STAMPS (measurement probes only; every schedule of the library has it
 // off, and split must be 1): each wave records the 100 MHz real-time counter
 // at entry, at the end of its K loop, once the partial tiles are in LDS,

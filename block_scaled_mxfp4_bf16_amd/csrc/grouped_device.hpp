@@ -9,24 +9,40 @@
 //   scales  quad q, K step ks: 256 bytes at (q * KS + ks) * 256, dword L the
 //           scale bytes of operand lane L of the quad's four tiles.
 // Tiles without a row are never written nor read.
+//
+// The product walks over "units", runs of 16, 64 or 128 rows of one expert,
+// that the first launch lists in the workspace: the group sizes are known on
+// the device only, and one 16-byte entry is cheaper for a workgroup to read
+// than E offsets to scan.
 #pragma once
 
 #include "experts_device.hpp"
+#include "experts_internal.hpp"
 
 namespace mxfp4 {
 
-// A run of rows of one group.
+// plan[0].x is the number of units, plan[1 + u] unit u.
 struct Unit {
-  int expert;  // -1: no such unit
-  int row;     // first output row
-  int rows;    // output rows from `row` to the end of the group
-  int tile;    // its first 16-row tile in the workspace
+  int expert;
+  int row;   // first output row
+  int rows;  // output rows from `row` to the end of the group
+  int tile;  // its first 16-row tile in the workspace
 };
 
-__device__ __forceinline__ void group_range(const int32_t *offsets, int e, int R, int &lo, int &hi) {
-  const int a = offsets[e], b = offsets[e + 1];
-  lo = a < 0 ? 0 : (a > R ? R : a);
-  hi = b < lo ? lo : (b > R ? R : b);
+// Entries are read through the scalar cache: the index is the same in every
+// lane, and the reads do not queue behind the operand loads.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Unit plan_entry(const GroupedArgs &a, int i) {
+  const i32x4 v = ((const __attribute__((address_space(4))) i32x4 *)a.plan)[i];
+  return Unit{v.x, v.y, v.z, v.w};
+}
+
+// Rows of expert e, clamped to [0, R): whatever the offsets hold, no group
+// reaches outside the output.
+__device__ __forceinline__ void group_range(const GroupedArgs &a, int e, int &lo, int &hi) {
+  const int p = a.offsets[e], q = a.offsets[e + 1];
+  lo = p < 0 ? 0 : (p > a.R ? a.R : p);
+  hi = q < lo ? lo : (q > a.R ? a.R : q);
 }
 
 __device__ __forceinline__ int wave_scan(int v, int lane) {
@@ -38,60 +54,96 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
   return v;
 }
 
-// Finds units of UR rows (a multiple of 16): every lane of a wave adds up the
-// units and quads of its share of the experts, and a scan over the lanes says
-// where each share starts.  All offsets are clamped to [0, R], so no group
-// reaches outside the output whatever they hold.
-template <int UR>
-struct UnitFinder {
-  int lane, per, first_e, last_e;
-  int units_before, quads_before, total;
-  const int32_t *offsets;
-  int R;
+// One wave's view of the groups: each lane holds the sums over its share of
+// the experts, a scan over the lanes says where the share starts.
+struct GroupScan {
+  int first_e, last_e;         // this lane's experts
+  int units_before, quads_before;
+  int units, quads;            // of all experts
 
-  __device__ __forceinline__ UnitFinder(const int32_t *off, int E, int R_, int lane_) : lane(lane_), offsets(off), R(R_) {
-    per = (E + 63) >> 6;
-    first_e = lane * per < E ? lane * per : E;
-    last_e = first_e + per < E ? first_e + per : E;
+  __device__ __forceinline__ GroupScan(const GroupedArgs &a, int lane) {
+    const int per = (a.E + 63) >> 6;
+    first_e = lane * per < a.E ? lane * per : a.E;
+    last_e = first_e + per < a.E ? first_e + per : a.E;
     int u = 0, q = 0;
     for (int e = first_e; e < last_e; ++e) {
       int lo, hi;
-      group_range(offsets, e, R, lo, hi);
-      u += (hi - lo + UR - 1) / UR;
+      group_range(a, e, lo, hi);
+      u += (hi - lo + a.unit_rows - 1) >> a.unit_shift;
       q += (hi - lo + 63) >> 6;
     }
     const int ui = wave_scan(u, lane), qi = wave_scan(q, lane);
     units_before = ui - u;
     quads_before = qi - q;
-    total = __builtin_amdgcn_readlane(ui, 63);
+    units = __builtin_amdgcn_readlane(ui, 63);
+    quads = __builtin_amdgcn_readlane(qi, 63);
   }
 
-  // index < total, the same in every lane
-  __device__ __forceinline__ Unit find(int index) const {
-    int e_found = -1, row = 0, rows = 0, tile = 0;
+  // The quad with the given index (below `quads`, the same in every lane).
+  __device__ __forceinline__ Unit quad(const GroupedArgs &a, int index) const {
+    int expert = -1, row = 0, rows = 0;
+    int q = quads_before;
+    for (int e = first_e; e < last_e; ++e) {
+      int lo, hi;
+      group_range(a, e, lo, hi);
+      const int n = (hi - lo + 63) >> 6;
+      if (index >= q && index < q + n) {
+        expert = e;
+        row = lo + (index - q) * 64;
+        rows = hi - row;
+      }
+      q += n;
+    }
+    const int src = __builtin_ctzll(__ballot(expert >= 0) | (1ull << 63));
+    return Unit{__builtin_amdgcn_readlane(expert, src), __builtin_amdgcn_readlane(row, src),
+                __builtin_amdgcn_readlane(rows, src), index * 4};
+  }
+
+  // Lists the units.  Offsets that do not rise can describe more units and
+  // quads than R rows can take; what lies past the workspace is left out.
+  __device__ __forceinline__ void list(const GroupedArgs &a, int lane) const {
     int u = units_before, q = quads_before;
     for (int e = first_e; e < last_e; ++e) {
       int lo, hi;
-      group_range(offsets, e, R, lo, hi);
-      const int n = (hi - lo + UR - 1) / UR;
-      if (index >= u && index < u + n) {
-        const int skip = (index - u) * UR;
-        e_found = e;
-        row = lo + skip;
-        rows = hi - row;
-        tile = q * 4 + (skip >> 4);
+      group_range(a, e, lo, hi);
+      const int last_quad = q + ((hi - lo + 63) >> 6);
+      for (int row = lo, tile = 4 * q; row < hi; row += a.unit_rows, tile += a.unit_rows >> 4, ++u) {
+        const bool fits = last_quad <= a.quads;
+        if (u < a.max_units) a.plan[1 + u] = int4{fits ? e : -1, row, fits ? hi - row : 0, tile};
       }
-      u += n;
-      q += (hi - lo + 63) >> 6;
+      q = last_quad;
     }
-    const int src = __builtin_ctzll(__ballot(e_found >= 0) | (1ull << 63));
-    Unit r;
-    r.expert = __builtin_amdgcn_readlane(e_found, src);
-    r.row = __builtin_amdgcn_readlane(row, src);
-    r.rows = __builtin_amdgcn_readlane(rows, src);
-    r.tile = __builtin_amdgcn_readlane(tile, src);
-    return r;
+    if (lane == 0) a.plan[0] = int4{units < a.max_units ? units : a.max_units, 0, 0, 0};
   }
 };
+
+__device__ __forceinline__ v4f mfma_fp4(const u32x4 &a, const u32x4 &b, const v4f &c, uint32_t sa, uint32_t sb) {
+  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// As above with the scales in byte `ia` of sa and `ib` of sb: the instruction
+// takes the byte numbers as constants, which they are once loops are unrolled.
+template <int IA>
+__device__ __forceinline__ v4f mfma_fp4_at(const v8i &a, const v8i &b, const v4f &c, uint32_t sa, uint32_t sb, int ib) {
+  switch (ib) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 3, (int)sb);
+  }
+}
+__device__ __forceinline__ v4f mfma_fp4_sel2(const u32x4 &a, const u32x4 &b, const v4f &c, uint32_t sa, int ia,
+                                             uint32_t sb, int ib) {
+  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  switch (ia) {
+    case 0: return mfma_fp4_at<0>(av, bv, c, sa, sb, ib);
+    case 1: return mfma_fp4_at<1>(av, bv, c, sa, sb, ib);
+    case 2: return mfma_fp4_at<2>(av, bv, c, sa, sb, ib);
+    default: return mfma_fp4_at<3>(av, bv, c, sa, sb, ib);
+  }
+}
 
 }  // namespace mxfp4

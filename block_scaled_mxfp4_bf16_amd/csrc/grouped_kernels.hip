@@ -5,22 +5,31 @@
 // Two launches.  The first gathers the rows of each group, quantizes them and
 // writes them in the layout that the matrix instruction takes, so that the
 // second reads every operand as whole 1 KiB blocks.  The group sizes stay on
-// the device: each workgroup finds its rows from the offsets by a scan over
-// the experts, and the grids are sized for the worst case.
-#include "experts_internal.hpp"
+// the device: the first launch finds its rows from the offsets by a scan over
+// the experts and lists the units of work for the second; grids are sized for
+// the worst case.
 #include "grouped_device.hpp"
-#include "mxfp4_internal.hpp"
+#include "grouped_tile.hpp"
 
 namespace mxfp4 {
 
-// Quads that R rows in E groups can take at most: every group wastes less
-// than one, and no more groups have rows than there are rows.
-static int64_t grouped_quads(int64_t R, int64_t E) { return (R + 63 * (E < R ? E : R)) / 64; }
+namespace {
 
-static int64_t k_steps(int64_t K) { return (K + 127) / 128; }
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// Units of `rows` rows that R rows in E groups can make at most: every group
+// wastes less than one, and no more groups have rows than there are rows.
+int64_t most_units(int64_t R, int64_t E, int64_t rows) { return (R + (rows - 1) * least(E, R)) / rows; }
+
+int64_t k_steps(int64_t K) { return (K + 127) / 128; }
+
+// Workspace: the list of units (16 rows each at most), codes, scales.
+int64_t plan_bytes(int64_t R, int64_t E) { return (16 * (1 + most_units(R, E, 16)) + 255) / 256 * 256; }
+
+}  // namespace
 
 size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E) {
-  return (size_t)grouped_quads(R, E) * (size_t)k_steps(K) * (4096 + 256);
+  return (size_t)(plan_bytes(R, E) + most_units(R, E, 64) * k_steps(K) * (4096 + 256));
 }
 
 // Gather and quantize.  One wave takes one K step of a quad, four waves the
@@ -32,24 +41,30 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KS = (a.K + 127) >> 7;
-  const UnitFinder<64> finder(a.offsets, a.E, a.R, lane);
+  const GroupScan groups(a, lane);
+
+  // one more workgroup lists the units
+  if ((int)blockIdx.x == a.quads) {
+    if (blockIdx.y == 0 && wave == 0) groups.list(a, lane);
+    return;
+  }
 
   // output rows of no group are zero
   if (blockIdx.y == 0) {
     int lo, hi, unused;
-    group_range(a.offsets, 0, a.R, lo, unused);
-    group_range(a.offsets, a.E - 1, a.R, unused, hi);
+    group_range(a, 0, lo, unused);
+    group_range(a, a.E - 1, unused, hi);
     const int cols = a.gated ? a.N >> 1 : a.N;
     const int outside = lo + (a.R - hi);
-    for (int i = blockIdx.x; i < outside; i += gridDim.x) {
+    for (int i = blockIdx.x; i < outside; i += a.quads) {
       uint16_t *c = a.C + (int64_t)(i < lo ? i : hi + i - lo) * a.ldc;
       for (int n = threadIdx.x; n < cols; n += 256) c[n] = 0;
     }
   }
 
   const int quad = blockIdx.x;
-  if (quad >= finder.total) return;
-  const Unit u = finder.find(quad);
+  if (quad >= groups.quads) return;
+  const Unit u = groups.quad(a, quad);
   const int ks = blockIdx.y * 4 + wave;
   if (u.expert < 0 || ks >= KS) return;
 
@@ -92,12 +107,6 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a) {
   ((uint32_t *)(a.scales + ((int64_t)(u.tile >> 2) * KS + ks) * 256))[c * 16 + (lane >> 2)] = d;
 }
 
-__device__ __forceinline__ v4f mfma_fp4(const u32x4 &a, const u32x4 &b, const v4f &c, uint32_t sa, uint32_t sb) {
-  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
 // Workgroup: 16 * MT rows of one group x 16 * NT columns, all of K; wave w
 // takes steps w, w + WK, ... with D steps in flight.  With `gated` the first
 // NT / 2 subtiles are gate columns and the others their up columns.
@@ -107,14 +116,12 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q4 = lane >> 4;
-  const UnitFinder<16 * MT> finder(a.offsets, a.E, a.R, lane);
-  const int64_t work = (int64_t)finder.total * n_tiles;
+  const int64_t work = (int64_t)plan_entry(a, 0).expert * n_tiles;
   for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
     const int index = (int)(item / n_tiles);
     const int n_tile = (int)(item - (int64_t)index * n_tiles);
-    const Unit u = finder.find(index);
-    // only offsets that are no offsets lead past the packed rows
-    if (u.expert < 0 || (u.tile >> 2) + (MT + 3) / 4 > a.quads) return;
+    const Unit u = plan_entry(a, 1 + index);
+    if (u.expert < 0) continue;
 
     const int N = a.N, K = a.K;
     const int KS = (K + 127) >> 7;
@@ -241,22 +248,35 @@ static hipError_t run_stream(const GroupedArgs &a, hipStream_t stream) {
   const int cols = a.gated ? 8 * NT : 16 * NT;
   const int out_cols = a.gated ? a.N >> 1 : a.N;
   const int n_tiles = (out_cols + cols - 1) / cols;
-  const int64_t units = ((int64_t)a.R + (int64_t)(16 * MT - 1) * (a.E < a.R ? a.E : a.R)) / (16 * MT);
-  const int64_t items = units * n_tiles;
-  grouped_stream_kernel<MT, NT, WK, D>
-      <<<(unsigned)(items < kMaxGrid ? items : kMaxGrid), 64 * WK, 0, stream>>>(a, n_tiles);
+  const int64_t items = (int64_t)a.max_units * n_tiles;
+  grouped_stream_kernel<MT, NT, WK, D><<<(unsigned)least(items, kMaxGrid), 64 * WK, 0, stream>>>(a, n_tiles);
+  return hipGetLastError();
+}
+
+static hipError_t run_tile(const GroupedArgs &a, hipStream_t stream) {
+  const int wide = ((uintptr_t)a.C & 7) == 0 && a.ldc % 4 == 0;
+  if (a.gated)
+    grouped_tile_kernel<true><<<512, 256, 0, stream>>>(a, (a.N / 2 + 127) / 128, wide);
+  else
+    grouped_tile_kernel<false><<<512, 256, 0, stream>>>(a, (a.N + 255) / 256, wide);
   return hipGetLastError();
 }
 
 hipError_t launch_grouped(GroupedArgs a, hipStream_t stream) {
-  const int64_t quads = grouped_quads(a.R, a.E), KS = k_steps(a.K);
+  const int64_t quads = most_units(a.R, a.E, 64), KS = k_steps(a.K);
+  const int64_t mean = a.R / least(a.E, a.R);  // rows of a group, were they even
+  const bool tile = mean > 64 && a.N % (a.gated ? 64 : 32) == 0;
+  a.unit_shift = tile ? 7 : (mean <= 16 ? 4 : 6);
+  a.unit_rows = 1 << a.unit_shift;
+  a.max_units = (int)most_units(a.R, a.E, a.unit_rows);
   a.quads = (int)quads;
-  a.codes = a.ws;
-  a.scales = a.ws + quads * KS * 4096;
-  pack_rows_kernel<<<dim3((unsigned)quads, (unsigned)((KS + 3) / 4)), 256, 0, stream>>>(a);
+  a.plan = (int4 *)a.ws;
+  a.codes = a.ws + plan_bytes(a.R, a.E);
+  a.scales = a.codes + quads * KS * 4096;
+  pack_rows_kernel<<<dim3((unsigned)quads + 1, (unsigned)((KS + 3) / 4)), 256, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t mean = a.R / (a.E < a.R ? a.E : a.R);  // rows of a group, were they even
+  if (tile) return run_tile(a, stream);
   if (mean <= 16) return run_stream<1, 2, 8, 2>(a, stream);
   return run_stream<4, 4, 4, 2>(a, stream);
 }

@@ -144,6 +144,21 @@ __device__ __forceinline__ int off_or_oob(bool in_range, int off) {
   return off | (in_range ? 0 : (int)0x80000000u);
 }
 
+// Uniform part of a buffer offset, moved out of range (bit 31) unless
+// `in_range`; the lane's part is added to it afterwards (all offsets stay
+// below 2^31, so the sum is out of range exactly when the flag is set).
+__device__ __forceinline__ int uniform_off(bool in_range, int off) {
+  return off | (in_range ? 0 : (int)0x80000000u);
+}
+
+// s_waitcnt for vmcnt <= N, expcnt and lgkmcnt left alone (gfx9 encoding:
+// vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N <= 63, "vmcnt is six bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
 // DPP lane patterns within groups of four lanes.
 constexpr int kQuadSwap1 = 0xB1;  // quad_perm [1, 0, 3, 2]
 constexpr int kQuadSwap2 = 0x4E;  // quad_perm [2, 3, 0, 1]
