@@ -10,6 +10,7 @@ functions raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -108,10 +109,27 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """Handle of torch's current stream on the current device.
+
+    torch.cuda.current_stream() builds a Stream object, 2.9 us a call; the two
+    calls underneath it take 0.2 us together."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # initializes torch's GPU state
+        device, stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = (lambda: stream(device())) if device and stream else \
+            (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -307,6 +325,9 @@ def gemm(A, Bw, Bs, N: int, out=None, stream=None):
 
 
 # ---- expert operators --------------------------------------------------------
+#
+# The checks below read each property of a tensor once: a call on one token
+# takes its time on the host, and every property costs 50-150 ns.
 
 MXFP4_TYPE_BF16, MXFP4_TYPE_F16, MXFP4_TYPE_F32 = 0, 1, 2
 
@@ -318,40 +339,52 @@ def _type(t):
     if not _types:
         import torch
         _types.update({torch.bfloat16: MXFP4_TYPE_BF16, torch.float16: MXFP4_TYPE_F16, torch.float32: MXFP4_TYPE_F32})
-    try:
-        return _types[t.dtype]
-    except KeyError:
-        raise TypeError("expected a bf16, f16 or f32 tensor, got %s" % t.dtype) from None
+    r = _types.get(t.dtype)
+    if r is None:
+        raise TypeError("expected a bf16, f16 or f32 tensor, got %s" % t.dtype)
+    return r
 
 
-def _int32(t, what, n, like):
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n or t.device != like.device:
-        raise ValueError("%s must be a contiguous int32 tensor of %d elements on %s" % (what, n, like.device))
+def _array(t, dtype, what, n, dev):
+    if t.dtype != dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (what, dtype, n, _device(dev)))
 
 
-def _rows_of(t, what, rows, cols, like):
-    """Checks a [rows, cols] tensor whose rows are contiguous; rows may be None."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != cols or t.device != like.device \
-            or (cols > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be a [%s, %d] tensor on %s with contiguous rows" %
-                         (what, "rows" if rows is None else rows, cols, like.device))
+def _device(dev):
+    return "cuda:%d" % dev if dev >= 0 else "the cpu"
 
 
-def _prepared(Bw, Bs, N, K, like):
+def _rows_of(t, what, rows, cols, dev):
+    """Row stride of a [rows, cols] tensor whose rows are contiguous; rows may be None."""
+    shape = t.shape
+    if len(shape) == 2 and (rows is None or shape[0] == rows) and shape[1] == cols and t.get_device() == dev:
+        ld, step = t.stride()
+        if step == 1 or cols <= 1:
+            return ld if shape[0] > 1 else cols
+    raise ValueError("%s must be a [%s, %d] tensor on %s with contiguous rows" %
+                     (what, "rows" if rows is None else rows, cols, _device(dev)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prepared_bytes(N, K):
+    return mxfp4_packed_bytes(N, K), mxfp4_shuffled_scale_bytes(N, K)
+
+
+def _prepared(Bw, Bs, N, K, dev):
     """Number of matrices in prepared codes and scales; checks their sizes."""
-    per_w, per_s = mxfp4_packed_bytes(N, K), mxfp4_shuffled_scale_bytes(N, K)
-    E = Bw.numel() // per_w if per_w else 0
-    if E < 1 or Bw.numel() != E * per_w or Bs.numel() != E * per_s or Bw.element_size() != 1 or Bs.element_size() != 1 \
-            or not Bw.is_contiguous() or not Bs.is_contiguous() or Bw.device != like.device or Bs.device != like.device:
+    per_w, per_s = _prepared_bytes(N, K)
+    total = Bw.numel()
+    E = total // per_w if per_w else 0
+    if E < 1 or total != E * per_w or Bs.numel() != E * per_s or Bw.itemsize != 1 or Bs.itemsize != 1 \
+            or not Bw.is_contiguous() or not Bs.is_contiguous() or Bw.get_device() != dev or Bs.get_device() != dev:
         raise ValueError("Bw and Bs must be contiguous byte tensors of prepared [%d, %d] matrices on %s" %
-                         (N, K, like.device))
+                         (N, K, _device(dev)))
     return E
 
 
-def _on_gpu(t):
-    if not t.is_cuda:
-        raise ValueError("the expert operators take cuda tensors, not %s ones" % t.device)
+def _on_gpu(dev):
+    if dev < 0:
+        raise ValueError("the expert operators take cuda tensors")
 
 
 def prepare_experts(B, stream=None):
@@ -376,25 +409,32 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
     none of them is zero.  gated: N/2 columns, silu(first half) * second.
     y's type is out's, else out_dtype, else x's."""
     import torch
-    K = x.shape[1]
-    _rows_of(x, "x", None, K, x)
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    tokens, K = x.shape
+    dev = x.get_device()
+    ldx = _rows_of(x, "x", None, K, dev)
     xt = _type(x)
-    E = _prepared(Bw, Bs, N, K, x)
-    M = x.shape[0] * repeat
+    E = _prepared(Bw, Bs, N, K, dev)
+    M = tokens * repeat
     if ids is not None:
-        _int32(ids, "ids", M, x)
+        _array(ids, torch.int32, "ids", M, dev)
+        ids = ids.data_ptr()
     elif E != 1:
         raise ValueError("%d matrices need ids" % E)
     cols = N // 2 if gated else N
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or x.dtype, device=x.device)
+        ldy = cols
     else:
-        _rows_of(out, "out", M, cols, x)
-    _on_gpu(x)
-    if M == 0:
-        return out
-    mxfp4_gemv(x, xt, x.stride(0) if x.shape[0] > 1 else K, Bw, Bs, ids, E, out, _type(out),
-               out.stride(0) if M > 1 else cols, M, N, K, repeat, gated, stream)
+        ldy = _rows_of(out, "out", M, cols, dev)
+    yt = _type(out)
+    _on_gpu(dev)
+    if M:
+        rc = _load().mxfp4_gemv(x.data_ptr(), xt, ldx, Bw.data_ptr(), Bs.data_ptr(), ids, E, out.data_ptr(), yt, ldy, M, N,
+                                K, repeat, 1 if gated else 0, _current_stream() if stream is None else _stream(stream))
+        if rc:
+            _check(rc, "mxfp4_gemv")
     return out
 
 
@@ -409,26 +449,32 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
     if A.dim() != 2:
         raise ValueError("A must be [rows, K]")
     T, K = A.shape
-    _rows_of(A, "A", T, K, A)
+    dev = A.get_device()
+    lda = _rows_of(A, "A", T, K, dev)
     if A.dtype != torch.bfloat16:
         raise TypeError("A must be bf16, not %s" % A.dtype)
-    E = _prepared(Bw, Bs, N, K, A)
-    _int32(offsets, "offsets", E + 1, A)
+    E = _prepared(Bw, Bs, N, K, dev)
+    _array(offsets, torch.int32, "offsets", E + 1, dev)
     if rows is not None:
-        _int32(rows, "rows", rows.numel(), A)
         R = rows.numel()
+        _array(rows, torch.int32, "rows", R, dev)
+        rows = rows.data_ptr()
     else:
         R = T
     cols = N // 2 if gated else N
     if out is None:
         out = torch.empty((R, cols), dtype=torch.bfloat16, device=A.device)
+        ldc = cols
     else:
-        _rows_of(out, "out", R, cols, A)
+        ldc = _rows_of(out, "out", R, cols, dev)
         if out.dtype != torch.bfloat16:
             raise TypeError("out must be bf16, not %s" % out.dtype)
-    _on_gpu(A)
-    mxfp4_gemm_grouped(A, A.stride(0) if T > 1 else K, T, Bw, Bs, E, offsets, rows, repeat, out,
-                       out.stride(0) if R > 1 else cols, R, N, K, gated, stream=stream)
+    _on_gpu(dev)
+    rc = _load().mxfp4_gemm_grouped(A.data_ptr(), lda, T, Bw.data_ptr(), Bs.data_ptr(), E, offsets.data_ptr(), rows, repeat,
+                                    out.data_ptr(), ldc, R, N, K, 1 if gated else 0, None, 0,
+                                    _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_gemm_grouped")
     return out
 
 
@@ -451,34 +497,35 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    _rows_of(logits, "logits", T, E, logits)
+    dev = logits.get_device()
+    ld = _rows_of(logits, "logits", T, E, dev)
     lt = _type(logits)
-    if score not in _scores:
+    kind = _scores.get(score)
+    if kind is None:
         raise ValueError("score must be 'softmax' or 'sigmoid', not %r" % (score,))
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous()
-                             or bias.device != logits.device):
-        raise ValueError("bias must be a contiguous f32 tensor of %d elements on %s" % (E, logits.device))
+    if bias is not None:
+        _array(bias, torch.float32, "bias", E, dev)
+        bias = bias.data_ptr()
+    n = T * k
     if out is None:
         i32 = dict(dtype=torch.int32, device=logits.device)
         out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=logits.device),
-               torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32))
+               torch.empty(E + 1, **i32), torch.empty(n, **i32), torch.empty((T, k), **i32))
+        ids, weights, offsets, rows, pos = out
     else:
         ids, weights, offsets, rows, pos = out
-        _int32(ids, "ids", T * k, logits)
-        _weights(weights, T, k, logits)
-        _int32(offsets, "offsets", E + 1, logits)
-        _int32(rows, "rows", T * k, logits)
-        _int32(pos, "pos", T * k, logits)
-    _on_gpu(logits)
-    mxfp4_moe_route(logits, lt, logits.stride(0) if T > 1 else E, bias, T, E, k, _scores[score], renormalize, *out,
-                    stream=stream)
+        _array(ids, torch.int32, "ids", n, dev)
+        _array(weights, torch.float32, "weights", n, dev)
+        _array(offsets, torch.int32, "offsets", E + 1, dev)
+        _array(rows, torch.int32, "rows", n, dev)
+        _array(pos, torch.int32, "pos", n, dev)
+    _on_gpu(dev)
+    rc = _load().mxfp4_moe_route(logits.data_ptr(), lt, ld, bias, T, E, k, kind, 1 if renormalize else 0, ids.data_ptr(),
+                                 weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), None, 0,
+                                 _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_moe_route")
     return out
-
-
-def _weights(t, T, k, like):
-    import torch
-    if t.dtype != torch.float32 or t.shape != (T, k) or not t.is_contiguous() or t.device != like.device:
-        raise ValueError("weights must be a contiguous f32 [%d, %d] tensor on %s" % (T, k, like.device))
 
 
 def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, stream=None):
@@ -493,24 +540,31 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
         raise ValueError("y must be [rows, N] and weights [T, k]")
     R, N = y.shape
     T, k = weights.shape
-    _rows_of(y, "y", R, N, y)
+    dev = y.get_device()
+    ld_y = _rows_of(y, "y", R, N, dev)
     yt = _type(y)
-    _weights(weights, T, k, y)
+    _array(weights, torch.float32, "weights", T * k, dev)
     if pos is not None:
-        _int32(pos, "pos", T * k, y)
+        _array(pos, torch.int32, "pos", T * k, dev)
+        pos = pos.data_ptr()
     elif R < T * k:
         raise ValueError("y has %d rows, %d tokens of %d choices need %d" % (R, T, k, T * k))
     if out is None:
         dtype = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
         out = torch.empty((T, N), dtype=dtype, device=y.device)
+        ld_out = N
     else:
-        _rows_of(out, "out", T, N, y)
+        ld_out = _rows_of(out, "out", T, N, dev)
+    ld_res = N
     if residual is not None:
-        _rows_of(residual, "residual", T, N, y)
+        ld_res = _rows_of(residual, "residual", T, N, dev)
         if residual.dtype != out.dtype:
             raise TypeError("residual is %s, out %s" % (residual.dtype, out.dtype))
-    _on_gpu(y)
-    mxfp4_moe_combine(y, yt, y.stride(0) if R > 1 else N, R, weights, pos, residual,
-                      residual.stride(0) if residual is not None and T > 1 else N, out, _type(out),
-                      out.stride(0) if T > 1 else N, T, k, N, stream=stream)
+        residual = residual.data_ptr()
+    ot = _type(out)
+    _on_gpu(dev)
+    rc = _load().mxfp4_moe_combine(y.data_ptr(), yt, ld_y, R, weights.data_ptr(), pos, residual, ld_res, out.data_ptr(), ot,
+                                   ld_out, T, k, N, _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_moe_combine")
     return out
