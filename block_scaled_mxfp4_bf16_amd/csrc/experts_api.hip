@@ -84,7 +84,7 @@ mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const
   a.offsets = offsets;
   a.rows = rows;
   a.pos = pos;
-  a.hist = (int32_t *)ws;
+  a.hist = (uint16_t *)ws;
   return hip_status(launch_route(a, (hipStream_t)stream));
 }
 

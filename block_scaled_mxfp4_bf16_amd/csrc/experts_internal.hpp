@@ -39,8 +39,8 @@ struct RouteArgs {
   int32_t *ids;
   float *weights;
   int32_t *offsets, *rows, *pos;
-  int32_t *hist;  // [blocks, E] counts, unless T is small
-  int blocks, per_block;
+  uint16_t *hist;  // [E][2^hist_shift] counts of each block, unless T is small
+  int blocks, per_block, hist_shift;
 };
 
 size_t route_workspace_bytes(int64_t T, int64_t E);

@@ -10,8 +10,9 @@
 // The choice is made on whole numbers: a value maps to an unsigned integer of
 // the same order, so the largest is a plain integer maximum.  Without a bias
 // the logits themselves order the experts (both scores rise with the logit);
-// with one, g + bias is formed in f64, since two f32 sums that round to the
-// same value would pick the wrong expert.  L lanes share a token, L = 16
+// with one, an f32 estimate of g + bias orders them, and wherever two are
+// closer than its error the f64 values decide, since two f32 sums that round
+// to the same value would pick the wrong expert.  L lanes share a token, L = 16
 // wherever E <= 256 and k <= 16: a maximum over 16 lanes is four rotate steps
 // and serves four tokens of a wave at once.  The weights of the k chosen are
 // computed in f64, one lane each, and rounded once.
@@ -80,84 +81,121 @@ __device__ __forceinline__ float logit(const RouteArgs &a, int64_t row, int e) {
 
 __device__ __forceinline__ bool lowest(float v) { return v == -__builtin_inff(); }
 
-enum { kPlain = 0, kSum = 1, kBias = 2 };
+// Value of an integer of order_of(float), never 0.
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
 
 // One token by the L lanes of the caller's group (V experts a lane, expert
-// l + L * v).  Lane j < k returns choice j.  kSum: the softmax's sum over all
-// experts is needed; kBias: g + bias orders them.
-template <int L, int V, int MODE>
+// l + L * v).  Lane j < k returns choice j.
+template <int L, int V, bool BIAS>
 __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l, int *id_out, float *w_out) {
-  using Key = typename std::conditional<MODE == kBias, uint64_t, uint32_t>::type;
   const auto larger = [](auto p, auto q) { return p > q ? p : q; };
   const auto smaller = [](int p, int q) { return p < q ? p : q; };
-  const auto plus = [](double p, double q) { return p + q; };
-  float x[V];
+  const auto plus = [](auto p, auto q) { return p + q; };
+  const bool softmax = a.score == MXFP4_SCORE_SOFTMAX;
+  float x[V], bias[BIAS ? V : 1];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = l + L * v;
     x[v] = e < a.E ? logit(a, t, e) : -__builtin_inff();
+    if constexpr (BIAS) bias[v] = e < a.E ? a.bias[e] : 0.f;
   }
-  float top = 0.f;
-  double total = 1.0;
-  Key key[V];
-  if constexpr (MODE != kPlain) {
-    if (a.score == MXFP4_SCORE_SOFTMAX) {
-      float m = x[0];
+  float top = 0.f;  // of the softmax
+  if (softmax) {
+    top = x[0];
 #pragma unroll
-      for (int v = 1; v < V; ++v) m = larger(m, x[v]);
-      top = all_reduce<L>(m, larger);
-      if (lowest(top)) top = 0.f;
-    }
-    double g[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      g[v] = a.score == MXFP4_SCORE_SOFTMAX ? exp((double)x[v] - top) : 1.0 / (1.0 + exp(-(double)x[v]));
-    if (a.score == MXFP4_SCORE_SOFTMAX) {
-      double s = g[0];
-#pragma unroll
-      for (int v = 1; v < V; ++v) s += g[v];
-      total = all_reduce<L>(s, plus);
-    }
-    if constexpr (MODE == kBias) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = l + L * v;
-        const float b = e < a.E ? a.bias[e] : 0.f;
-        const double by = (a.score == MXFP4_SCORE_SOFTMAX ? g[v] / total : g[v]) + b;
-        key[v] = lowest(x[v]) || lowest(b) || b != b ? 0 : order_of(by);
-      }
-    }
+    for (int v = 1; v < V; ++v) top = larger(top, x[v]);
+    top = all_reduce<L>(top, larger);
+    if (lowest(top)) top = 0.f;
   }
-  if constexpr (MODE != kBias) {
+  const auto sum64 = [&]() {
+    double s = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s += exp((double)x[v] - top);
+    return all_reduce<L>(s, plus);
+  };
+  // renormalized weights need no sum over all experts
+  const double total = softmax && !a.renorm ? sum64() : 1.0;
+
+  // Without a bias the key is the logit's own.  With one it is that of an f32
+  // estimate of g + bias, off by less than `slack` / 2: the exponential and
+  // quotient of g by less than 2^-21, the sum of E <= 1024 terms in a softmax
+  // by less than 2^-19 of g <= 1, the addition by 2^-24 of the result.
+  uint32_t key[V];
+  if constexpr (BIAS) {
+    float g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = softmax ? __expf(x[v] - top) : 1.0f / (1.0f + __expf(-x[v]));
+    float scale = 1.f;
+    if (softmax) {
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) s += g[v];
+      s = all_reduce<L>(s, plus);
+      scale = s > 0.f ? 1.0f / s : 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool dead = lowest(x[v]) || lowest(bias[v]) || bias[v] != bias[v];
+      key[v] = dead ? 0 : order_of(__builtin_fminf(g[v] * scale + bias[v], 3.402823466e38f));
+    }
+  } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = lowest(x[v]) ? 0 : order_of(x[v]);
   }
 
   int id = -1;
+  double sum_all = 0.0;  // of the softmax, once two estimates are too close
   for (int j = 0; j < a.k; ++j) {
-    Key m = key[0];
+    uint32_t m = key[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = larger(m, key[v]);
     m = all_reduce<L>(m, larger);
-    int c = INT32_MAX;
+    uint32_t near = m;  // keys from here on may be the largest
+    if constexpr (BIAS) {
+      const float top_value = value_of(m ? m : 0x80000000u);
+      near = order_of(top_value - (0x1p-18f + 0x1p-22f * __builtin_fabsf(top_value)));
+      near = m ? (near ? near : 1u) : 0u;
+    }
+    int c = INT32_MAX, c_last = -1;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) c = key[v] == m ? l + L * v : c;
+    for (int v = V - 1; v >= 0; --v) {
+      const bool is = key[v] >= near;
+      c = is ? l + L * v : c;
+      if constexpr (BIAS) c_last = is ? larger(c_last, l + L * v) : c_last;
+    }
     c = all_reduce<L>(c, smaller);
+    if constexpr (BIAS) {
+      c_last = all_reduce<L>(c_last, larger);
+      if (__ballot(m && c != c_last)) {
+        // more than one candidate in some token of the wave: decide by f64
+        if (softmax && sum_all == 0.0) sum_all = sum64();
+        uint64_t best = 0;
+        int at = INT32_MAX;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (__ballot(m && key[v] >= near)) {
+            const double g = softmax ? exp((double)x[v] - top) / sum_all : 1.0 / (1.0 + exp(-(double)x[v]));
+            const uint64_t o = m && key[v] >= near ? order_of(g + bias[v]) : 0;
+            at = o > best ? l + L * v : at;
+            best = larger(best, o);
+          }
+        }
+        const uint64_t all = all_reduce<L>(best, larger);
+        const int exact = all_reduce<L>(best == all ? at : INT32_MAX, smaller);
+        c = m ? exact : c;
+      }
+    }
     if (l == j) id = m ? c : -1;
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = l + L * v == c ? 0 : key[v];
-    if constexpr (MODE == kPlain) {
-      if (j == 0 && a.score == MXFP4_SCORE_SOFTMAX) {  // the first choice is the largest logit
-        const uint32_t o = m;
-        top = m ? __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu)) : 0.f;
-      }
-    }
   }
 
   double w = 0.0;
   if (id >= 0) {
     const double xl = (double)logit(a, t, id);
-    w = a.score == MXFP4_SCORE_SOFTMAX ? exp(xl - top) / total : 1.0 / (1.0 + exp(-xl));
+    w = softmax ? exp(xl - top) / total : 1.0 / (1.0 + exp(-xl));
   }
   if (a.renorm) {
     const double s = all_reduce<L>(w, plus);
@@ -169,13 +207,13 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
 
 // Tokens [t0, t1) by the block's groups of L lanes: ids and weights, and the
 // count of each expert in `hist` (zeroed by the caller).
-template <int L, int V, int MODE, int THREADS>
+template <int L, int V, bool BIAS, int THREADS>
 __device__ __forceinline__ void route_tokens(const RouteArgs &a, int64_t t0, int64_t t1, int *hist) {
   const int l = threadIdx.x & (L - 1);
   for (int64_t t = t0 + threadIdx.x / L; t < t1; t += THREADS / L) {
     int id;
     float w;
-    route_token<L, V, MODE>(a, t, l, &id, &w);
+    route_token<L, V, BIAS>(a, t, l, &id, &w);
     if (l < a.k) {
       a.ids[t * a.k + l] = id;
       a.weights[t * a.k + l] = w;
@@ -262,40 +300,62 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int6
 }  // namespace
 
 // First launch of many tokens: block b takes tokens [b * per_block, ...) and
-// leaves its expert counts in hist[b].
-template <int L, int V, int MODE>
-__global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a) {
+// leaves its count of expert e in hist[e][b] (16 bits: a token takes an expert
+// once, and a block has at most 4096 tokens).
+template <int L, int V, bool BIAS>
+__global__ __launch_bounds__(512) void route_choose_kernel(const RouteArgs a) {
   __shared__ int hist[kMaxExperts];
-  for (int e = threadIdx.x; e < a.E; e += 256) hist[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += 512) hist[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * a.per_block;
-  route_tokens<L, V, MODE, 256>(a, t0, t0 + a.per_block < a.T ? t0 + a.per_block : a.T, hist);
+  route_tokens<L, V, BIAS, 512>(a, t0, t0 + a.per_block < a.T ? t0 + a.per_block : a.T, hist);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 256) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+  for (int e = threadIdx.x; e < a.E; e += 512) a.hist[((int64_t)e << a.hist_shift) + blockIdx.x] = (uint16_t)hist[e];
 }
 
 // Second launch: the same blocks add up the counts before theirs and place
-// their pairs.
-__global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a) {
+// their pairs.  Every block reads all counts, 16 bytes (8 blocks of one
+// expert) a load, 8 loads in flight: one a lane and dependent, as in a plain
+// loop, they took 30 us of the 35 of 256 blocks of 128 experts.
+__global__ __launch_bounds__(512) void route_place_kernel(const RouteArgs a) {
   __shared__ int next[kMaxExperts];    // all counts, then first place, of each expert
   __shared__ int before[kMaxExperts];  // pairs of the expert in earlier blocks
-  __shared__ int wave_next[4][kMaxExperts];
+  __shared__ int wave_next[8][kMaxExperts];
   __shared__ int used;
-  for (int e = threadIdx.x; e < a.E; e += 256) next[e] = before[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += 512) next[e] = before[e] = 0;
   __syncthreads();
-  // `seg` threads share an expert's counts, each taking every seg-th block
-  int width = 1;
-  while (width < a.E && width < 256) width <<= 1;
-  const int seg = 256 / width;
-  for (int e = threadIdx.x & (width - 1); e < a.E; e += width) {
-    int all = 0, mine = 0;
-    for (int b = threadIdx.x / width; b < a.blocks; b += seg) {
-      const int c = a.hist[(int64_t)b * a.E + e];
-      all += c;
-      mine += b < (int)blockIdx.x ? c : 0;
+  // 16 lanes share an expert where it has 16 chunks of 8 blocks or more
+  const int per_expert = a.hist_shift - 3;  // log2 of its chunks
+  const int chunks = a.E << per_expert;
+  for (int c0 = 0; c0 < chunks; c0 += 512 * 8) {
+    u32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + 512 * i + threadIdx.x;
+      v[i] = c < chunks ? ((const u32x4 *)a.hist)[c] : u32x4{0, 0, 0, 0};
     }
-    atomicAdd(&next[e], all);
-    atomicAdd(&before[e], mine);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + 512 * i + threadIdx.x;
+      const int e = c >> per_expert;
+      const int b0 = (c - (e << per_expert)) * 8;
+      int all = 0, mine = 0;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const int n = (v[i][h >> 1] >> (16 * (h & 1))) & 0xFFFF;
+        all += b0 + h < a.blocks ? n : 0;
+        mine += b0 + h < (int)blockIdx.x ? n : 0;
+      }
+      if (per_expert >= 4) {
+        all = all_reduce<16>(all, [](int p, int q) { return p + q; });
+        mine = all_reduce<16>(mine, [](int p, int q) { return p + q; });
+        if ((threadIdx.x & 15) != 0) continue;
+      }
+      if (c < chunks) {
+        atomicAdd(&next[e], all);
+        atomicAdd(&before[e], mine);
+      }
+    }
   }
   __syncthreads();
   if (threadIdx.x < 64) {
@@ -304,28 +364,28 @@ __global__ __launch_bounds__(256) void route_place_kernel(const RouteArgs a) {
   }
   __syncthreads();
   if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e < a.E; e += 256) a.offsets[e] = next[e];
+    for (int e = threadIdx.x; e < a.E; e += 512) a.offsets[e] = next[e];
     if (threadIdx.x == 0) a.offsets[a.E] = used;
   }
   const int64_t pairs = (int64_t)a.T * a.k;
-  for (int64_t p = used + (int64_t)blockIdx.x * 256 + threadIdx.x; p < pairs; p += (int64_t)a.blocks * 256)
+  for (int64_t p = used + (int64_t)blockIdx.x * 512 + threadIdx.x; p < pairs; p += (int64_t)a.blocks * 512)
     a.rows[p] = -1;
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 256) next[e] += before[e];
+  for (int e = threadIdx.x; e < a.E; e += 512) next[e] += before[e];
   const int64_t p0 = (int64_t)blockIdx.x * a.per_block * a.k;
   const int64_t p1 = p0 + (int64_t)a.per_block * a.k;
-  place_pairs<256>(a, p0, p1 < pairs ? p1 : pairs, next, wave_next);
+  place_pairs<512>(a, p0, p1 < pairs ? p1 : pairs, next, wave_next);
 }
 
 // Few tokens: all of it in one workgroup and one launch.
-template <int L, int V, int MODE>
+template <int L, int V, bool BIAS>
 __global__ __launch_bounds__(512) void route_small_kernel(const RouteArgs a) {
   __shared__ int next[kMaxExperts];
   __shared__ int wave_next[8][kMaxExperts];
   __shared__ int used;
   for (int e = threadIdx.x; e < a.E; e += 512) next[e] = 0;
   __syncthreads();
-  route_tokens<L, V, MODE, 512>(a, 0, a.T, next);
+  route_tokens<L, V, BIAS, 512>(a, 0, a.T, next);
   __syncthreads();  // the ids this block wrote are read back below
   if (threadIdx.x < 64) {
     const int n = scan_experts(next, a.E);
@@ -345,43 +405,49 @@ constexpr int kSmallTokens = 128;
 // Tokens per block otherwise: at most 256 blocks, whole passes of 16 tokens.
 static int64_t route_per_block(int64_t T) { return ((T + 255) / 256 + 15) / 16 * 16; }
 
-size_t route_workspace_bytes(int64_t T, int64_t E) {
-  if (T <= kSmallTokens) return 0;
-  const int64_t per = route_per_block(T);
-  return (size_t)((T + per - 1) / per * E * 4);
+// log2 of the places per expert in the counts: a power of two that holds all
+// blocks, 8 at least.
+static int route_hist_shift(int64_t T) {
+  const int64_t per = route_per_block(T), blocks = (T + per - 1) / per;
+  int s = 3;
+  while ((1 << s) < blocks) ++s;
+  return s;
 }
 
-template <int L, int V, int MODE>
+size_t route_workspace_bytes(int64_t T, int64_t E) {
+  return T <= kSmallTokens ? 0 : (size_t)(E << route_hist_shift(T)) * 2;
+}
+
+template <int L, int V, bool BIAS>
 static hipError_t run_route(RouteArgs a, hipStream_t stream) {
   if (a.T <= kSmallTokens) {
-    route_small_kernel<L, V, MODE><<<1, 512, 0, stream>>>(a);
+    route_small_kernel<L, V, BIAS><<<1, 512, 0, stream>>>(a);
     return hipGetLastError();
   }
   a.per_block = (int)route_per_block(a.T);
   a.blocks = (a.T + a.per_block - 1) / a.per_block;
-  route_choose_kernel<L, V, MODE><<<a.blocks, 256, 0, stream>>>(a);
+  a.hist_shift = route_hist_shift(a.T);
+  route_choose_kernel<L, V, BIAS><<<a.blocks, 512, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  route_place_kernel<<<a.blocks, 256, 0, stream>>>(a);
+  route_place_kernel<<<a.blocks, 512, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int MODE>
-static hipError_t run_route_mode(const RouteArgs &a, hipStream_t stream) {
+template <bool BIAS>
+static hipError_t run_route_layout(const RouteArgs &a, hipStream_t stream) {
   if (a.k <= 16) {
-    if (a.E <= 64) return run_route<16, 4, MODE>(a, stream);
-    if (a.E <= 128) return run_route<16, 8, MODE>(a, stream);
-    if (a.E <= 256) return run_route<16, 16, MODE>(a, stream);
+    if (a.E <= 64) return run_route<16, 4, BIAS>(a, stream);
+    if (a.E <= 128) return run_route<16, 8, BIAS>(a, stream);
+    if (a.E <= 256) return run_route<16, 16, BIAS>(a, stream);
   } else if (a.E <= 256) {
-    return run_route<32, 8, MODE>(a, stream);
+    return run_route<32, 8, BIAS>(a, stream);
   }
-  return run_route<64, 16, MODE>(a, stream);
+  return run_route<64, 16, BIAS>(a, stream);
 }
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-  if (a.bias) return run_route_mode<kBias>(a, stream);
-  if (a.score == MXFP4_SCORE_SOFTMAX && !a.renorm) return run_route_mode<kSum>(a, stream);
-  return run_route_mode<kPlain>(a, stream);
+  return a.bias ? run_route_layout<true>(a, stream) : run_route_layout<false>(a, stream);
 }
 
 }  // namespace mxfp4

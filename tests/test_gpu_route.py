@@ -209,3 +209,21 @@ def test_other_streams_and_graphs():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1e-7, 1.0, 1e6, 3e38])
+def test_close_sums_and_far_biases(score, scale):
+    """Biases so close that f32 estimates cannot tell the sums apart, or so far that they drown the scores."""
+    torch = torch_cuda()
+    T, E, k = 200, 72, 9
+    l = logits_of(torch, 31, T, E, "bf16", 1e-3)
+    bias = logits_of(torch, 32, 1, E, "f32", 1.0).reshape(-1).clamp(-1, 1) * scale
+    bias[3] = float("inf")
+    check(torch, l, k, score, bias, True, "scale %g" % scale)
+
+
+@pytest.mark.parametrize("T", [20000, 70001])
+def test_many_tokens(T):
+    torch = torch_cuda()
+    check(torch, logits_of(torch, T, T, 40, "bf16"), 3, "sigmoid", torch.linspace(0, 0.1, 40).cuda(), what="many")
