@@ -36,8 +36,6 @@ namespace {
 
 enum { kBf16 = 0, kF16 = 1, kF32 = 2 };
 
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-
 // Eight weights of one dword of codes as bf16, scaled by a power of two.
 __device__ __forceinline__ bf16x8 weights_bf16(uint32_t w, float scale) {
   union {
@@ -61,19 +59,6 @@ __device__ __forceinline__ f16x8 weights_f16(uint32_t w) {
   u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
   u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
   return u.v;
-}
-
-// Swap the upper 32 lanes of a with the lower 32 of b.
-__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {
-  const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r.x;
-  b = r.y;
-}
-// Swap lanes 16-31 of a with lanes 0-15 of b, and 48-63 with 32-47.
-__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
-  const u32x2 r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r.x;
-  b = r.y;
 }
 
 // Eight f32 values as three bf16 vectors whose sum is exact: each part is

@@ -254,11 +254,11 @@ static hipError_t run_stream(const GroupedArgs &a, hipStream_t stream) {
 }
 
 static hipError_t run_tile(const GroupedArgs &a, hipStream_t stream) {
-  const int wide = ((uintptr_t)a.C & 7) == 0 && a.ldc % 4 == 0;
+  const int wide = ((uintptr_t)a.C & 15) == 0 && a.ldc % 8 == 0;
   if (a.gated)
-    grouped_tile_kernel<true><<<512, 256, 0, stream>>>(a, (a.N / 2 + 127) / 128, wide);
+    grouped_tile_kernel<true, 1><<<512, 256, 0, stream>>>(a, (a.N / 2 + 127) / 128, wide);
   else
-    grouped_tile_kernel<false><<<512, 256, 0, stream>>>(a, (a.N + 255) / 256, wide);
+    grouped_tile_kernel<false, 1><<<512, 256, 0, stream>>>(a, (a.N + 255) / 256, wide);
   return hipGetLastError();
 }
 

@@ -4,7 +4,7 @@
 //
 // The four waves share the 128 rows and split the columns, 64 each, so
 //   - a block of weights is needed by one wave only and goes from memory to
-//     its registers, four K steps ahead;
+//     its registers, three K steps ahead;
 //   - the rows go through LDS, one 8 KiB slot per K step written directly by
 //     the memory system, four slots in a ring; LDS then serves 40 KiB a step
 //     and workgroup, where staging the weights as well would take 72 and make
@@ -29,19 +29,21 @@ __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <bool GATED>
-__global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs a, int n_tiles, int wide_stores) {
+template <bool GATED, int WM>
+__global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const GroupedArgs a, int n_tiles, int wide_stores) {
   constexpr int MT = 8, NT = 4;
+  constexpr int UT = MT * WM;  // 16-row tiles of a unit
   constexpr int BN = GATED ? 128 : 256;  // output columns of a tile
-  constexpr int kNowhere = (int)0x80000000u;  // an offset that every buffer ends below
-  __shared__ __attribute__((aligned(16))) uint8_t slot0[MT * 1024];
-  __shared__ __attribute__((aligned(16))) uint8_t slot1[MT * 1024];
-  __shared__ __attribute__((aligned(16))) uint8_t slot2[MT * 1024];
-  __shared__ __attribute__((aligned(16))) uint8_t slot3[MT * 1024];
+  constexpr int STORES = MT * (GATED ? NT / 2 : NT) / 2;  // of a wave and tile, 16 bytes a lane
+  __shared__ __attribute__((aligned(16))) uint8_t slot0[UT * 1024];
+  __shared__ __attribute__((aligned(16))) uint8_t slot1[UT * 1024];
+  __shared__ __attribute__((aligned(16))) uint8_t slot2[UT * 1024];
+  __shared__ __attribute__((aligned(16))) uint8_t slot3[UT * 1024];
   const auto slot = [&](int s) -> uint8_t * { return s == 0 ? slot0 : (s == 1 ? slot1 : (s == 2 ? slot2 : slot3)); };
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
   const int l16 = lane * 16, l4 = lane * 4;
   const int N = a.N, K = a.K;
   const int KS = (K + 127) >> 7;
@@ -62,12 +64,15 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
   int next_item = (int)((int64_t)items * xcd >> 3) + (blockIdx.x >> 3);
   if (next_item >= end) return;
 
-  // What the loads of a tile need.  `none` (no tile left) has empty buffers.
-  __amdgpu_buffer_rsrc_t a_rsrc, as_rsrc, b_rsrc, s_rsrc;
-  int b_off, s_off;    // byte offsets of the wave's first group and its scales
-  int b_off2, s_off2;  // the same of its second pair of groups (the up columns)
-  Unit unit;           // of the tile that the loads are in
-  int col0;            // its first output column of this wave
+  // What the loads of a tile need.  Offsets that all lanes share go into the
+  // instructions' scalar offset, which the range check includes: an offset at
+  // the end of a buffer or past it reads zeros, as does a buffer of size 0 (no
+  // tile left, a tile of no rows, a step past K).
+  const uint8_t *a_base, *as_base, *b_base, *s_base;
+  int a_size, as_size, b_size, s_size;
+  int b_off[2], s_off[2];  // of the wave's two pairs of 16-row groups, and of their scales
+  Unit unit;               // of the tile that the loads are in
+  int col0;                // its first output column of this wave
   bool none;
 
   auto enter = [&]() {
@@ -76,61 +81,69 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
     const int n_tile = none ? 0 : next_item - u * n_tiles;
     next_item += stride;
     unit = plan_entry(a, 1 + u);
-    const int tiles = none || unit.expert < 0 ? 0 : (unit.rows < 128 ? (unit.rows + 15) >> 4 : MT);
+    const int tiles = none || unit.expert < 0 ? 0 : (unit.rows < 16 * UT ? (unit.rows + 15) >> 4 : UT);
     const int64_t expert = unit.expert < 0 ? 0 : unit.expert;
-    a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(a.codes + (int64_t)unit.tile * KS * 1024), 0,
-                                               tiles * KS * 1024, kRsrcWord3);
-    as_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(a.scales + (int64_t)(unit.tile >> 2) * KS * 256), 0,
-                                                ((tiles + 3) >> 2) * KS * 256, kRsrcWord3);
-    b_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(a.Bw + expert * b_bytes), 0, tiles ? b_bytes : 0, kRsrcWord3);
-    s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(a.Bs + expert * s_bytes), 0, tiles ? s_bytes : 0, kRsrcWord3);
-    col0 = n_tile * BN + wave * (BN / 4);
+    a_size = tiles * KS * 1024;
+    as_size = ((tiles + 3) >> 2) * KS * 256;
+    b_size = tiles > MT * wm ? b_bytes : 0;  // a wave without rows needs no weights
+    s_size = tiles > MT * wm ? s_bytes : 0;
+    a_base = a.codes + (int64_t)unit.tile * KS * 1024;
+    as_base = a.scales + (int64_t)(unit.tile >> 2) * KS * 256;
+    b_base = a.Bw + expert * b_bytes;
+    s_base = a.Bs + expert * s_bytes;
+    col0 = n_tile * BN + wn * (BN / 4);
     const int g = col0 >> 4;
     const int up = GATED ? N >> 5 : 2;
-    const bool ok1 = GATED ? g < (N >> 5) : g < (N >> 4);
-    const bool ok2 = GATED ? ok1 : g + 2 < (N >> 4);
-    b_off = ok1 ? g * K * 8 : kNowhere;
-    b_off2 = ok2 ? (g + up) * K * 8 : kNowhere;
-    s_off = ok1 ? (g >> 1) * gp * 32 : kNowhere;
-    s_off2 = ok2 ? ((g + up) >> 1) * gp * 32 : kNowhere;
+    const bool ok0 = GATED ? g < (N >> 5) : g < (N >> 4);
+    const bool ok1 = GATED ? ok0 : g + 2 < (N >> 4);
+    b_off[0] = ok0 ? g * K * 8 : b_bytes;
+    b_off[1] = ok1 ? (g + up) * K * 8 : b_bytes;
+    s_off[0] = ok0 ? (g >> 1) * gp * 32 : s_bytes;
+    s_off[1] = ok1 ? ((g + up) >> 1) * gp * 32 : s_bytes;
+  };
+  const auto sized = [](const uint8_t *base, int size) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, size, kRsrcWord3);
   };
 
-  // Rows of step ks of the loads' tile into slot s: two of its eight blocks by
-  // each wave.
-  auto load_rows = [&](int ks, int s) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = 2 * wave + i;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          a_rsrc, (__attribute__((address_space(3))) void *)(slot(s) + t * 1024), 16,
-          uniform_off(ks < KS, (t * KS + ks) * 1024) + l16, 0, 0, 0);
-    }
-  };
   struct Stage {
     u32x4 b[NT];
     uint32_t as[2];
     uint32_t bs[2];  // of an even step and the next one; unused in odd stages
   };
   Stage st[4];
-  auto load_weights = [&](int ks, int s) {
-    const bool ok = ks < KS;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      st[s].b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
-          b_rsrc, uniform_off(ok, (nt < 2 ? b_off : b_off2) + (nt & 1) * K * 8 + ks * 1024) + l16, 0, 0);
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      st[s].as[q] = __builtin_amdgcn_raw_buffer_load_b32(as_rsrc, uniform_off(ok, (q * KS + ks) * 256) + l4, 0, 0);
-    if (s & 1) {
+  // Part p of the loads of step k0 + s of the loads' tile, into slot and stage
+  // s; the eight parts go out between the products of a step, since a wave
+  // that issues them in one run waits for the address unit (16 cycles a KiB)
+  // and leaves the matrix unit idle.
+  auto load_part = [&](int k0, int s, int p) {
+    const bool ok = k0 + s < KS;
+    if (p == 0) {
       // the weights' scales of this step and the one before, whose stage is
       // loaded but not yet in use; at an odd step the old ones are done with
+      const bool any = k0 + s - 1 < KS;
+      if (s & 1)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          st[s - 1].bs[q] = __builtin_amdgcn_raw_buffer_load_b32(sized(s_base, any ? s_size : 0), l4 + (s >> 1) * 256,
+                                                                 s_off[q] + k0 * 128, 0);
+    } else if (p < 3) {  // rows: two of their blocks by each wave
+      const int t = 2 * wave + p - 1;
+      const __amdgpu_buffer_rsrc_t r = sized(a_base, ok ? a_size : 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(slot(s) + t * 1024), 16, l16,
+                                               (t * KS + k0 + s) * 1024, 0, 0);
+    } else if (p < 7) {
+      const int nt = p - 3;
+      st[s].b[nt] = __builtin_amdgcn_raw_buffer_load_b128(sized(b_base, ok ? b_size : 0), l16 + s * 1024,
+                                                          b_off[nt >> 1] + (nt & 1) * K * 8 + k0 * 1024, 0);
+    } else {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        st[s - 1].bs[q] = __builtin_amdgcn_raw_buffer_load_b32(
-            s_rsrc, uniform_off(ks - 1 < KS, (q ? s_off2 : s_off) + (ks >> 1) * 256) + l4, 0, 0);
+        st[s].as[q] = __builtin_amdgcn_raw_buffer_load_b32(sized(as_base, ok ? as_size : 0), l4 + s * 256,
+                                                           ((2 * wm + q) * KS + k0) * 256, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  auto row_block = [&](int s, int mt) { return *(const u32x4 *)(slot(s) + mt * 1024 + l16); };
+  auto row_block = [&](int s, int mt) { return *(const u32x4 *)(slot(s) + (wm * MT + mt) * 1024 + l16); };
 
   v4f acc[MT][NT];
   auto clear = [&]() {
@@ -140,76 +153,101 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
       for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
   };
   auto store = [&](const Unit &u, int col, auto wide) {
-    const int rows = u.expert < 0 ? 0 : (u.rows < 128 ? u.rows : 128);
+    const int row0 = 16 * MT * wm;
+    const int left = u.expert < 0 ? 0 : u.rows - row0;
+    const int rows = left < 0 ? 0 : (left < 16 * MT ? left : 16 * MT);
     const int ldc = (int)a.ldc * 2;
     const __amdgpu_buffer_rsrc_t c_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(a.C + (int64_t)u.row * a.ldc), 0, rows ? (rows - 1) * ldc + out_cols * 2 : 0, kRsrcWord3);
-    const int at = (lane & 15) * ldc + (col + (lane >> 4) * 4) * 2;
+        (void *)(a.C + (int64_t)(u.row + row0) * a.ldc), 0, rows ? (rows - 1) * ldc + out_cols * 2 : 0, kRsrcWord3);
+    const int row = lane & 15, q4 = lane >> 4;
+    // A lane holds columns 4 q4 .. 4 q4 + 3 of its row in each subtile.  A swap
+    // between the lane quarters of two neighbouring subtiles leaves it with
+    // eight neighbouring columns: of the first subtile in even quarters, of the
+    // second in odd ones.  A store then covers 64 contiguous bytes of each of
+    // 16 rows; 8 bytes a lane straight from the accumulators left the kernel
+    // (32768 rows, 4096 x 2048, gated) 40 us slower than no stores at all.
+    const int at = row * ldc + (col + 16 * (q4 & 1) + 4 * (q4 & 2)) * 2;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const bool row_ok = 16 * mt + (lane & 15) < rows;
+      const bool row_ok = 16 * mt + row < rows;
 #pragma unroll
-      for (int nt = 0; nt < (GATED ? NT / 2 : NT); ++nt) {
-        float v[4];
+      for (int nt = 0; nt < (GATED ? NT / 2 : NT); nt += 2) {
+        uint32_t d[2][2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = GATED ? gated_silu(acc[mt][nt][r], acc[mt][(nt + 2) % NT][r]) : acc[mt][nt][r];
-        const bool ok = row_ok && col + 16 * nt < out_cols;
-        const int off = off_or_oob(ok, at + 16 * mt * ldc + 32 * nt);
-        const uint32_t lo = bf16x2_rne(v[0], v[1]), hi = bf16x2_rne(v[2], v[3]);
+        for (int h = 0; h < 2; ++h) {
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[r] = GATED ? gated_silu(acc[mt][nt + h][r], acc[mt][(nt + h + 2) % NT][r]) : acc[mt][nt + h][r];
+          d[h][0] = bf16x2_rne(v[0], v[1]);
+          d[h][1] = bf16x2_rne(v[2], v[3]);
+        }
+        swap16(d[0][0], d[1][0]);
+        swap16(d[0][1], d[1][1]);
+        const int off = off_or_oob(row_ok && col + 16 * nt < out_cols, at + 16 * mt * ldc + 32 * nt);
         if constexpr (decltype(wide)::value) {
-          typedef uint32_t u32x2s __attribute__((ext_vector_type(2)));
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2s{lo, hi}, c_rsrc, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{d[0][0], d[0][1], d[1][0], d[1][1]}, c_rsrc, off, 0, 0);
         } else {
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)lo, c_rsrc, off, 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(lo >> 16), c_rsrc, off, 2, 0);
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)hi, c_rsrc, off, 4, 0);
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(hi >> 16), c_rsrc, off, 6, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = d[i >> 1][i & 1];
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, c_rsrc, off, 4 * i, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> 16), c_rsrc, off, 4 * i + 2, 0);
+          }
         }
       }
     }
   };
 
-  // Loads go out in this order, each step's weights (6 loads, 8 in odd steps)
-  // four steps and its rows (2 loads) three steps ahead:
-  //   step i: rows(i + 3), weights(i + 4); step i + 1: rows(i + 4), ...
-  // so at the start of step i the 16 newest loads came after rows(i + 1).
-  // The scheduling barriers keep the compiler from mixing the steps' loads:
+  // Loads go out three steps ahead, in step order: the weights' scales (2 loads,
+  // for odd steps), the rows (2), the weights and the rows' scales (6).  At the
+  // start of step i at least the 14 newest (16 if i is odd) came after
+  // rows(i + 1).  The scheduling barriers keep the compiler from mixing them:
   // the load counter retires in issue order.
   u32x4 x[4];
   enter();
-  load_rows(0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-  load_weights(0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-  load_weights(1, 1);
-  __builtin_amdgcn_sched_barrier(0);
-  load_rows(1, 1);
-  __builtin_amdgcn_sched_barrier(0);
-  load_weights(2, 2);
-  __builtin_amdgcn_sched_barrier(0);
-  load_rows(2, 2);
-  __builtin_amdgcn_sched_barrier(0);
-  load_weights(3, 3);
-  __builtin_amdgcn_sched_barrier(0);
-  wait_vmcnt<32>();
+#pragma unroll
+  for (int s = 0; s < 3; ++s)
+#pragma unroll
+    for (int p = 0; p < 8; ++p) load_part(0, s, p);
+  wait_vmcnt<24>();  // after the first rows: 6 + 2 + 2 + 6 + 2 + 6
   bare_barrier();
 #pragma unroll
   for (int i = 0; i < 3; ++i) x[i] = row_block(0, i);
   clear();
-  int ks = 0;  // first step of the round that the loads of slot 3 are in
+  int ks = 0;          // first step of the round that the loads of slot 3 are in
+  bool fresh = false;  // the first round after another tile's stores
   for (;;) {
     const bool last = ks + 4 >= steps;  // the last round of this tile
     const Unit tile_unit = unit;
     const int tile_col = col0;
+    const int live = tile_unit.expert < 0 ? 0 : (tile_unit.rows + 15 - 16 * MT * wm) >> 4;  // row tiles with a row
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // rows(i + 1) have arrived for every wave, and every wave has read
-      // rows(i - 1), whose slot the next load fills
+      // rows(i - 1), whose slot the next loads fill
       __builtin_amdgcn_sched_barrier(0);
-      wait_vmcnt<16>();
+      if (s == 0 && fresh)  // the last tile's stores came in between
+        wait_vmcnt<14 + STORES>();
+      else if (s == 1 && fresh)
+        wait_vmcnt<16 + STORES>();
+      else if (s & 1)
+        wait_vmcnt<16>();
+      else
+        wait_vmcnt<14>();
       bare_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      load_rows(s == 0 ? ks + 3 : ks + s - 1, (s + 3) & 3);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        x[(mt + 3) & 3] = mt + 3 < MT ? row_block(s, mt + 3) : row_block((s + 1) & 3, mt + 3 - MT);
+        if ((mt & ~3) < live)  // four tiles at a time: fewer conditions to keep
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            acc[mt][nt] = mfma_fp4_sel2(st[s].b[nt], x[mt & 3], acc[mt][nt], st[s & 2].bs[nt >> 1],
+                                        (nt & 1) + 2 * (s & 1), st[s].as[mt >> 2], mt & 3);
+        __builtin_amdgcn_sched_barrier(0);
+        load_part(ks, (s + 3) & 3, mt);
+      }
       if (s == 0) {
         ks += 4;
         if (last) {
@@ -217,17 +255,8 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
           enter();
         }
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        x[(mt + 3) & 3] = mt + 3 < MT ? row_block(s, mt + 3) : row_block((s + 1) & 3, mt + 3 - MT);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          acc[mt][nt] = mfma_fp4_sel2(st[s].b[nt], x[mt & 3], acc[mt][nt], st[s & 2].bs[nt >> 1], (nt & 1) + 2 * (s & 1),
-                                      st[s].as[mt >> 2], mt & 3);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      load_weights(ks + s, s);
     }
+    fresh = last;
     if (last) {
       if (wide_stores) {
         store(tile_unit, tile_col, std::true_type{});
