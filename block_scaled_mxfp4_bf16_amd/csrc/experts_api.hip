@@ -89,7 +89,7 @@ mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const
 }
 
 size_t mxfp4_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int64_t experts) {
-  if (R < 1 || K < 1 || experts < 1 || R > kMaxRows || K >= kMaxBytes || experts > kMaxGroups) return 0;
+  if (R < 1 || K < 1 || experts < 1 || R > kMaxRows || K > ((int64_t)1 << 17) || experts > kMaxGroups) return 0;
   return grouped_workspace_bytes(R, K, experts);
 }
 
@@ -102,7 +102,7 @@ mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, co
   if (lda < K || ldc < (gated ? N / 2 : N)) return MXFP4_ERR_INVALID_ARG;
   if (K % 32 != 0 || N % 16 != 0 || (gated && N % 32 != 0)) return MXFP4_ERR_UNSUPPORTED;
   if (R > kMaxRows || a_rows > kMaxRows || experts > kMaxGroups || repeat > INT32_MAX || !matrix_fits(N, K) ||
-      N > kMaxRows || lda > ((int64_t)1 << 30) || ldc > ((int64_t)1 << 22))
+      N > kMaxRows || K > ((int64_t)1 << 17) || lda > ((int64_t)1 << 30) || ldc > ((int64_t)1 << 22))
     return MXFP4_ERR_UNSUPPORTED;
   if (!aligned(A, 16) || lda % 8 != 0 || !aligned(Bq_sh, 16) || !aligned(Bs_sh, 16) || !aligned(offsets, 4) ||
       !aligned(rows, 4) || !aligned(C, 2))

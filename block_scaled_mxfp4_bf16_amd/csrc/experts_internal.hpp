@@ -60,6 +60,7 @@ struct GroupedArgs {
   int4 *plan;
   uint8_t *codes, *scales;
   int quads, max_units, unit_rows, unit_shift;
+  int pairs;  // the order of the packed rows' scales
 };
 
 size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E);

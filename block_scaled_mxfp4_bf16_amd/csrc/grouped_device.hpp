@@ -6,8 +6,10 @@
 // order, each quad in the operand layout of the large-M product:
 //   codes   16-row tile t, K step ks: 1 KiB at (t * KS + ks) * 1024, operand
 //           lane L's 16 bytes at 16 * L (row 16 t + L % 16, K chunk L / 16);
-//   scales  quad q, K step ks: 256 bytes at (q * KS + ks) * 256, dword L the
-//           scale bytes of operand lane L of the quad's four tiles.
+//   scales  quad q, K step ks: 256 bytes at (q * KS + ks) * 256.  For the
+//           16-row instruction dword L holds operand lane L's scale bytes of
+//           the quad's four tiles; for the 32-row one (`pairs`) byte 2 t + h of
+//           dword L is that of row 32 t + L % 32, K chunk 2 h + L / 32.
 // Tiles without a row are never written nor read.
 //
 // The product walks over "units", runs of 16, 64 or 128 rows of one expert,
@@ -45,12 +47,16 @@ __device__ __forceinline__ void group_range(const GroupedArgs &a, int e, int &lo
   hi = q < lo ? lo : (q > a.R ? a.R : q);
 }
 
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// Inclusive sums over the lanes of a wave: shifts by 1, 2, 4 and 8 within the
+// rows of 16 lanes, then the last lane of row 0 (2) added to row 1 (3) and that
+// of lane 31 to the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
   return v;
 }
 
@@ -72,7 +78,7 @@ struct GroupScan {
       u += (hi - lo + a.unit_rows - 1) >> a.unit_shift;
       q += (hi - lo + 63) >> 6;
     }
-    const int ui = wave_scan(u, lane), qi = wave_scan(q, lane);
+    const int ui = wave_scan(u), qi = wave_scan(q);
     units_before = ui - u;
     quads_before = qi - q;
     units = __builtin_amdgcn_readlane(ui, 63);
@@ -121,29 +127,6 @@ __device__ __forceinline__ v4f mfma_fp4(const u32x4 &a, const u32x4 &b, const v4
   const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// As above with the scales in byte `ia` of sa and `ib` of sb: the instruction
-// takes the byte numbers as constants, which they are once loops are unrolled.
-template <int IA>
-__device__ __forceinline__ v4f mfma_fp4_at(const v8i &a, const v8i &b, const v4f &c, uint32_t sa, uint32_t sb, int ib) {
-  switch (ib) {
-    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 0, (int)sb);
-    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 1, (int)sb);
-    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 2, (int)sb);
-    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 3, (int)sb);
-  }
-}
-__device__ __forceinline__ v4f mfma_fp4_sel2(const u32x4 &a, const u32x4 &b, const v4f &c, uint32_t sa, int ia,
-                                             uint32_t sb, int ib) {
-  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  switch (ia) {
-    case 0: return mfma_fp4_at<0>(av, bv, c, sa, sb, ib);
-    case 1: return mfma_fp4_at<1>(av, bv, c, sa, sb, ib);
-    case 2: return mfma_fp4_at<2>(av, bv, c, sa, sb, ib);
-    default: return mfma_fp4_at<3>(av, bv, c, sa, sb, ib);
-  }
 }
 
 }  // namespace mxfp4

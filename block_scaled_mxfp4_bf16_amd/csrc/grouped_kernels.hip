@@ -32,53 +32,59 @@ size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E) {
   return (size_t)(plan_bytes(R, E) + most_units(R, E, 64) * k_steps(K) * (4096 + 256));
 }
 
-// Gather and quantize.  One wave takes one K step of a quad, four waves the
-// steps of a workgroup.  Four lanes share a group of 32 elements (as in the
-// large-M product's quantizer), so a load covers 16 rows of 64 bytes; all 16
-// loads of a wave are issued before the first is used.  Rows past the group
-// and groups past K load as zeros and become zero codes with scale byte 0.
-__global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a) {
+// Gather and quantize.  One wave takes one K step of a quad, the four waves of
+// a workgroup four consecutive ones, and workgroups next to each other the
+// steps of one quad, so that rows are read in long runs.  Four lanes share a
+// group of 32 elements (as in the large-M product's quantizer), so a load
+// covers 16 rows of 64 bytes; all 16 loads of a wave are issued before the
+// first is used.  Rows past the group and groups past K load as zeros and
+// become zero codes with scale byte 0.
+__global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a, int runs) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KS = (a.K + 127) >> 7;
   const GroupScan groups(a, lane);
+  const int quad = blockIdx.x / runs;  // of `runs` workgroups each
+  const int run = blockIdx.x - quad * runs;
 
-  // one more workgroup lists the units
-  if ((int)blockIdx.x == a.quads) {
-    if (blockIdx.y == 0 && wave == 0) groups.list(a, lane);
+  // the first workgroup past the quads lists the units
+  if (quad == a.quads) {
+    if (run == 0 && wave == 0) groups.list(a, lane);
     return;
   }
 
   // output rows of no group are zero
-  if (blockIdx.y == 0) {
+  if (run == 0) {
     int lo, hi, unused;
     group_range(a, 0, lo, unused);
     group_range(a, a.E - 1, unused, hi);
     const int cols = a.gated ? a.N >> 1 : a.N;
     const int outside = lo + (a.R - hi);
-    for (int i = blockIdx.x; i < outside; i += a.quads) {
+    for (int i = quad; i < outside; i += a.quads) {
       uint16_t *c = a.C + (int64_t)(i < lo ? i : hi + i - lo) * a.ldc;
       for (int n = threadIdx.x; n < cols; n += 256) c[n] = 0;
     }
   }
 
-  const int quad = blockIdx.x;
   if (quad >= groups.quads) return;
   const Unit u = groups.quad(a, quad);
-  const int ks = blockIdx.y * 4 + wave;
+  const int ks = run * 4 + wave;
   if (u.expert < 0 || ks >= KS) return;
 
+  // the row of A of each of the quad's rows, one a lane
+  int from = -1;
+  if (lane < u.rows) {
+    const int p = u.row + lane;
+    from = a.rows ? a.rows[p] : p;
+    if (a.rows) from = from < 0 ? -1 : from / a.repeat;
+    if (from >= a.a_rows) from = -1;
+  }
   u32x4 w[4][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int r = 16 * j + (lane >> 2);
-    int64_t src = -1;
-    if (r < u.rows) {
-      const int p = u.row + r;
-      src = a.rows ? (a.rows[p] < 0 ? -1 : a.rows[p] / a.repeat) : p;
-    }
-    const bool ok = src >= 0 && src < a.a_rows;
-    const uint16_t *row = a.A + (ok ? src : 0) * a.lda;
+    const int src = __shfl(from, 16 * j + (lane >> 2));
+    const bool ok = src >= 0;
+    const uint16_t *row = a.A + (int64_t)(ok ? src : 0) * a.lda;
 #pragma unroll
     for (int ch = 0; ch < 4; ++ch) {
       const int k = ks * 128 + ch * 32 + (lane & 3) * 8;
@@ -103,7 +109,14 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a) {
   }
   // lane 4 * row + c writes the scales of operand lane 16 * c + row
   const int c = lane & 3;
-  const uint32_t d = c == 0 ? dw[0] : (c == 1 ? dw[1] : (c == 2 ? dw[2] : dw[3]));
+  uint32_t d;
+  if (a.pairs) {
+    // chunks c / 2 and c / 2 + 2 of blocks c % 2 and c % 2 + 2
+    const uint32_t first = (c & 2 ? dw[1] : dw[0]) >> (8 * (c & 1)), second = (c & 2 ? dw[3] : dw[2]) >> (8 * (c & 1));
+    d = (first & 0xFF) | ((second & 0xFF) << 8) | (first & 0xFF0000) | ((second & 0xFF0000) << 8);
+  } else {
+    d = c == 0 ? dw[0] : (c == 1 ? dw[1] : (c == 2 ? dw[2] : dw[3]));
+  }
   ((uint32_t *)(a.scales + ((int64_t)(u.tile >> 2) * KS + ks) * 256))[c * 16 + (lane >> 2)] = d;
 }
 
@@ -267,13 +280,15 @@ hipError_t launch_grouped(GroupedArgs a, hipStream_t stream) {
   const int64_t mean = a.R / least(a.E, a.R);  // rows of a group, were they even
   const bool tile = mean > 64 && a.N % (a.gated ? 64 : 32) == 0;
   a.unit_shift = tile ? 7 : (mean <= 16 ? 4 : 6);
+  a.pairs = tile;
   a.unit_rows = 1 << a.unit_shift;
   a.max_units = (int)most_units(a.R, a.E, a.unit_rows);
   a.quads = (int)quads;
   a.plan = (int4 *)a.ws;
   a.codes = a.ws + plan_bytes(a.R, a.E);
   a.scales = a.codes + quads * KS * 4096;
-  pack_rows_kernel<<<dim3((unsigned)quads + 1, (unsigned)((KS + 3) / 4)), 256, 0, stream>>>(a);
+  const int64_t runs = (KS + 3) / 4;
+  pack_rows_kernel<<<(unsigned)(quads * runs + 1), 256, 0, stream>>>(a, (int)runs);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (tile) return run_tile(a, stream);

@@ -29,12 +29,30 @@ __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// As mfma_fp4_sel2 for 32 x 32 outputs and 64 of K.
+typedef float v16f __attribute__((ext_vector_type(16)));
+template <int IA>
+__device__ __forceinline__ v16f mfma32_fp4_at(const v8i &a, const v8i &b, const v16f &c, uint32_t sa, uint32_t sb, int ib) {
+  switch (ib) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, IA, (int)sa, 3, (int)sb);
+  }
+}
+__device__ __forceinline__ v16f mfma32_fp4_sel2(const u32x4 &a, const u32x4 &b, const v16f &c, uint32_t sa, int ia,
+                                                uint32_t sb, int ib) {
+  const v8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return ia ? mfma32_fp4_at<2>(av, bv, c, sa, sb, ib) : mfma32_fp4_at<0>(av, bv, c, sa, sb, ib);
+}
+
 template <bool GATED, int WM>
 __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const GroupedArgs a, int n_tiles, int wide_stores) {
-  constexpr int MT = 8, NT = 4;
-  constexpr int UT = MT * WM;  // 16-row tiles of a unit
+  constexpr int MT = 4;          // 32-row tiles of a wave
+  constexpr int UT = 2 * MT * WM;  // 16-row blocks of a unit
   constexpr int BN = GATED ? 128 : 256;  // output columns of a tile
-  constexpr int STORES = MT * (GATED ? NT / 2 : NT) / 2;  // of a wave and tile, 16 bytes a lane
+  constexpr int STORES = MT * (GATED ? 2 : 4);  // of a wave and tile, 16 bytes a lane
   __shared__ __attribute__((aligned(16))) uint8_t slot0[UT * 1024];
   __shared__ __attribute__((aligned(16))) uint8_t slot1[UT * 1024];
   __shared__ __attribute__((aligned(16))) uint8_t slot2[UT * 1024];
@@ -45,6 +63,10 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int l16 = lane * 16, l4 = lane * 4;
+  // The 32x32x64 instruction takes row lane % 32 and K chunk lane / 32 of one
+  // half of a step; a 32-row tile is two blocks of 16 rows x 4 chunks.
+  const int r1 = (lane >> 4) & 1, hi = lane >> 5;
+  const int in_block = (lane & 15) * 16 + hi * 256;  // + 512 for the second half
   const int N = a.N, K = a.K;
   const int KS = (K + 127) >> 7;
   const int steps = (KS + 3) & ~3;  // steps past K load and add nothing
@@ -85,8 +107,8 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
     const int64_t expert = unit.expert < 0 ? 0 : unit.expert;
     a_size = tiles * KS * 1024;
     as_size = ((tiles + 3) >> 2) * KS * 256;
-    b_size = tiles > MT * wm ? b_bytes : 0;  // a wave without rows needs no weights
-    s_size = tiles > MT * wm ? s_bytes : 0;
+    b_size = tiles > 2 * MT * wm ? b_bytes : 0;  // a wave without rows needs no weights
+    s_size = tiles > 2 * MT * wm ? s_bytes : 0;
     a_base = a.codes + (int64_t)unit.tile * KS * 1024;
     as_base = a.scales + (int64_t)(unit.tile >> 2) * KS * 256;
     b_base = a.Bw + expert * b_bytes;
@@ -106,11 +128,12 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
   };
 
   struct Stage {
-    u32x4 b[NT];
-    uint32_t as[2];
-    uint32_t bs[2];  // of an even step and the next one; unused in odd stages
+    u32x4 b[2][2];    // [32-column tile][half of the step]
+    uint32_t as[2];   // of each 64 rows: byte 2 * (32-row tile) + half
+    uint32_t bs[2];   // of an even step and the next one, as prepared; unused in odd stages
   };
   Stage st[4];
+  const int b_lane = in_block + r1 * K * 8;
   // Part p of the loads of step k0 + s of the loads' tile, into slot and stage
   // s; the eight parts go out between the products of a step, since a wave
   // that issues them in one run waits for the address unit (16 cycles a KiB)
@@ -132,9 +155,9 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(slot(s) + t * 1024), 16, l16,
                                                (t * KS + k0 + s) * 1024, 0, 0);
     } else if (p < 7) {
-      const int nt = p - 3;
-      st[s].b[nt] = __builtin_amdgcn_raw_buffer_load_b128(sized(b_base, ok ? b_size : 0), l16 + s * 1024,
-                                                          b_off[nt >> 1] + (nt & 1) * K * 8 + k0 * 1024, 0);
+      const int nt = (p - 3) >> 1, h = (p - 3) & 1;
+      st[s].b[nt][h] = __builtin_amdgcn_raw_buffer_load_b128(sized(b_base, ok ? b_size : 0), b_lane + s * 1024 + h * 512,
+                                                             b_off[nt] + k0 * 1024, 0);
     } else {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -143,57 +166,72 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto row_block = [&](int s, int mt) { return *(const u32x4 *)(slot(s) + (wm * MT + mt) * 1024 + l16); };
+  // Rows 32 mt + lane % 32 of the wave, half h of the step in slot s.
+  auto row_block = [&](int s, int i) {
+    const int mt = i >> 1, h = i & 1;
+    return *(const u32x4 *)(slot(s) + (wm * 2 * MT + 2 * mt) * 1024 + h * 512 + r1 * 1024 + in_block);
+  };
 
-  v4f acc[MT][NT];
+  v16f acc[MT][2];
   auto clear = [&]() {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[mt][nt][i] = 0.f;
   };
   auto store = [&](const Unit &u, int col, auto wide) {
-    const int row0 = 16 * MT * wm;
+    const int row0 = 32 * MT * wm;
     const int left = u.expert < 0 ? 0 : u.rows - row0;
-    const int rows = left < 0 ? 0 : (left < 16 * MT ? left : 16 * MT);
+    const int rows = left < 0 ? 0 : (left < 32 * MT ? left : 32 * MT);
     const int ldc = (int)a.ldc * 2;
     const __amdgpu_buffer_rsrc_t c_rsrc = __builtin_amdgcn_make_buffer_rsrc(
         (void *)(a.C + (int64_t)(u.row + row0) * a.ldc), 0, rows ? (rows - 1) * ldc + out_cols * 2 : 0, kRsrcWord3);
-    const int row = lane & 15, q4 = lane >> 4;
-    // A lane holds columns 4 q4 .. 4 q4 + 3 of its row in each subtile.  A swap
-    // between the lane quarters of two neighbouring subtiles leaves it with
-    // eight neighbouring columns: of the first subtile in even quarters, of the
-    // second in odd ones.  A store then covers 64 contiguous bytes of each of
-    // 16 rows; 8 bytes a lane straight from the accumulators left the kernel
-    // (32768 rows, 4096 x 2048, gated) 40 us slower than no stores at all.
-    const int at = row * ldc + (col + 16 * (q4 & 1) + 4 * (q4 & 2)) * 2;
+    // Element 4 j + r of an accumulator is column 8 j + 4 * (lane / 32) + r of
+    // row lane % 32.  A swap of the upper half of the lanes in j = 2 p with the
+    // lower half in j = 2 p + 1 leaves each lane eight neighbouring columns,
+    // one 16-byte store.
+    // The lane number is found anew for each tile, from a zero that the
+    // compiler cannot see through: it would keep the offsets of every store
+    // through the products otherwise, and has no registers for them.
+    uint32_t zero = 0;
+    asm volatile("" : "+s"(zero));
+    const int me = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+    const int at = (me & 31) * ldc + (col + 8 * (me >> 5)) * 2;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const bool row_ok = 16 * mt + row < rows;
+      const bool row_ok = 32 * mt + (me & 31) < rows;
 #pragma unroll
-      for (int nt = 0; nt < (GATED ? NT / 2 : NT); nt += 2) {
-        uint32_t d[2][2];
+      for (int nt = 0; nt < (GATED ? 1 : 2); ++nt) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[4];
+        for (int p = 0; p < 2; ++p) {
+          uint32_t d[2][2];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            v[r] = GATED ? gated_silu(acc[mt][nt + h][r], acc[mt][(nt + h + 2) % NT][r]) : acc[mt][nt + h][r];
-          d[h][0] = bf16x2_rne(v[0], v[1]);
-          d[h][1] = bf16x2_rne(v[2], v[3]);
-        }
-        swap16(d[0][0], d[1][0]);
-        swap16(d[0][1], d[1][1]);
-        const int off = off_or_oob(row_ok && col + 16 * nt < out_cols, at + 16 * mt * ldc + 32 * nt);
-        if constexpr (decltype(wide)::value) {
-          __builtin_amdgcn_raw_buffer_store_b128(u32x4{d[0][0], d[0][1], d[1][0], d[1][1]}, c_rsrc, off, 0, 0);
-        } else {
+          for (int j = 0; j < 2; ++j) {
+            float v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w = d[i >> 1][i & 1];
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, c_rsrc, off, 4 * i, 0);
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> 16), c_rsrc, off, 4 * i + 2, 0);
+            for (int r = 0; r < 4; ++r) {
+              const int i = 8 * p + 4 * j + r;
+              v[r] = GATED ? gated_silu(acc[mt][0][i], acc[mt][1][i]) : acc[mt][nt][i];
+            }
+            d[j][0] = bf16x2_rne(v[0], v[1]);
+            d[j][1] = bf16x2_rne(v[2], v[3]);
           }
+          swap32(d[0][0], d[1][0]);
+          swap32(d[0][1], d[1][1]);
+          const int off = off_or_oob(row_ok && col + 32 * nt < out_cols, at + 32 * mt * ldc + 64 * nt + 32 * p);
+          if constexpr (decltype(wide)::value) {
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{d[0][0], d[0][1], d[1][0], d[1][1]}, c_rsrc, off, 0, 0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w = d[i >> 1][i & 1];
+              __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, c_rsrc, off, 4 * i, 0);
+              __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> 16), c_rsrc, off, 4 * i + 2, 0);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);  // few values at a time: the registers are full
         }
       }
     }
@@ -205,6 +243,7 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
   // rows(i + 1).  The scheduling barriers keep the compiler from mixing them:
   // the load counter retires in issue order.
   u32x4 x[4];
+  uint32_t wscale[2][2];
   enter();
 #pragma unroll
   for (int s = 0; s < 3; ++s)
@@ -221,7 +260,7 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
     const bool last = ks + 4 >= steps;  // the last round of this tile
     const Unit tile_unit = unit;
     const int tile_col = col0;
-    const int live = tile_unit.expert < 0 ? 0 : (tile_unit.rows + 15 - 16 * MT * wm) >> 4;  // row tiles with a row
+    const int live = tile_unit.expert < 0 ? 0 : tile_unit.rows - 32 * MT * wm;  // rows of this wave
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // rows(i + 1) have arrived for every wave, and every wave has read
@@ -237,16 +276,31 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
         wait_vmcnt<14>();
       bare_barrier();
       __builtin_amdgcn_sched_barrier(0);
+      // The prepared scale dwords hold, at lane 16 c + n, chunk c of columns n
+      // (byte 0, or 2 in odd steps) and 16 + n (byte 1 or 3).  Two swaps spread
+      // the chunks of each half over the lanes that the instruction takes them
+      // from, and a shift brings the lane's column to byte 0 or 2.
+      if ((s & 1) == 0) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        x[(mt + 3) & 3] = mt + 3 < MT ? row_block(s, mt + 3) : row_block((s + 1) & 3, mt + 3 - MT);
-        if ((mt & ~3) < live)  // four tiles at a time: fewer conditions to keep
+        for (int nt = 0; nt < 2; ++nt) {
+          wscale[nt][0] = wscale[nt][1] = st[s].bs[nt];
+          swap16(wscale[nt][0], wscale[nt][1]);
+          swap32(wscale[nt][0], wscale[nt][1]);
+          wscale[nt][0] >>= 8 * r1;
+          wscale[nt][1] >>= 8 * r1;
+        }
+      }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            acc[mt][nt] = mfma_fp4_sel2(st[s].b[nt], x[mt & 3], acc[mt][nt], st[s & 2].bs[nt >> 1],
-                                        (nt & 1) + 2 * (s & 1), st[s].as[mt >> 2], mt & 3);
+      for (int i = 0; i < 2 * MT; ++i) {
+        const int mt = i >> 1, h = i & 1;
+        x[(i + 3) & 3] = i + 3 < 2 * MT ? row_block(s, i + 3) : row_block((s + 1) & 3, i + 3 - 2 * MT);
+        if (64 * (mt >> 1) < live)  // 64 rows at a time: fewer conditions to keep
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+            acc[mt][nt] = mfma32_fp4_sel2(st[s].b[nt][h], x[i & 3], acc[mt][nt], wscale[nt][h], 2 * (s & 1),
+                                          st[s].as[mt >> 1], 2 * (mt & 1) + h);
         __builtin_amdgcn_sched_barrier(0);
-        load_part(ks, (s + 3) & 3, mt);
+        load_part(ks, (s + 3) & 3, i);
       }
       if (s == 0) {
         ks += 4;

@@ -379,7 +379,7 @@ MXFP4_API mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t
 /*         aligned, B not 16-byte aligned, C not 2-byte aligned);             */
 /*         UNSUPPORTED (K % 32 != 0, N % 16 != 0, gated with N % 32 != 0, a  */
 /*         matrix beyond 2^31 bytes, N, R or a_rows > 2^20, experts > 4096,    */
-/*         ldc > 2^22, lda > 2^30);                                           */
+/*         K > 2^17, ldc > 2^22, lda > 2^30);                                 */
 /*         WORKSPACE; HIP.                                                    */
 MXFP4_API size_t mxfp4_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int64_t experts);
 MXFP4_API mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, const void *Bq_sh,
