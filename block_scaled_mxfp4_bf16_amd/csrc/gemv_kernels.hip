@@ -94,15 +94,15 @@ __device__ __forceinline__ void split_f32(const u32x4 &p, const u32x4 &q, bf16x8
 
 }  // namespace
 
-// Workgroup: 16*MT rows (or, with ids, one row) x 16*NT columns, all of K;
+// Workgroup: 16 rows (or, with ids, one row) x 16*NT columns, all of K;
 // wave w takes steps w, w + WK, ... with D steps in flight.  With `gated`
 // the first NT/2 subtiles are gate columns and the others their up columns.
-template <int XT, int MT, int NT, int WK, int D>
+template <int XT, int NT, int WK, int D>
 __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
-  constexpr int XL = XT == kF32 ? 8 : 4;  // 16-byte loads of x per row tile and step
+  constexpr int XL = XT == kF32 ? 8 : 4;  // 16-byte loads of x per step
   constexpr int ES = XT == kF32 ? 4 : 2;  // bytes per element of x
   constexpr int NSD = NT > 1 ? NT : 1;
-  __shared__ __attribute__((aligned(16))) float red[WK * MT * NT * 256];
+  __shared__ __attribute__((aligned(16))) float red[WK * NT * 256];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   const int G = K >> 5;
   const int gp = (G + 7) & ~7;
 
-  int row0 = blockIdx.y * 16 * MT, rows = a.M - row0;
+  int row0 = blockIdx.y * 16, rows = a.M - row0;
   int64_t xrow = row0;
   const uint8_t *Bw = a.Bw, *Bs = a.Bs;
   const int out_cols = a.gated ? N >> 1 : N;
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
     Bw += e * b_bytes;
     Bs += e * s_bytes;
   }
-  if (rows > 16 * MT) rows = 16 * MT;
+  if (rows > 16) rows = 16;
 
   const uint8_t *x = (const uint8_t *)a.x + xrow * a.ldx * ES;
   const int ldx = (int)a.ldx * ES;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   }
 
   struct Stage {
-    u32x4 x[MT][XL];
+    u32x4 x[XL];
     u32x4 b[NT];
     uint32_t s[NSD];
   };
@@ -174,33 +174,24 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
           s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = 16 * mt + n16;
-#pragma unroll
-      for (int i = 0; i < XL; ++i) {
-        // first element of the 16 bytes, in the order the products take them
-        const int el = XT == kF16 ? i * 32 + q4 * 8 : q4 * 32 + i * (16 / ES);
-        const int g = 4 * ks + (XT == kF16 ? i : q4);
-        st.x[mt][i] = __builtin_amdgcn_raw_buffer_load_b128(
-            x_rsrc, off_or_oob(ok && r < rows && g < G, r * ldx + (ks * 128 + el) * ES), 0, 0);
-      }
+    for (int i = 0; i < XL; ++i) {
+      // first element of the 16 bytes, in the order the products take them
+      const int el = XT == kF16 ? i * 32 + q4 * 8 : q4 * 32 + i * (16 / ES);
+      const int g = 4 * ks + (XT == kF16 ? i : q4);
+      st.x[i] = __builtin_amdgcn_raw_buffer_load_b128(
+          x_rsrc, off_or_oob(ok && n16 < rows && g < G, n16 * ldx + (ks * 128 + el) * ES), 0, 0);
     }
   };
 
-  v4f acc[MT][NT];
+  v4f acc[NT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int nt = 0; nt < NT; ++nt) acc[nt] = v4f{0.f, 0.f, 0.f, 0.f};
 
   auto compute = [&](int ks, const Stage &st) {
-    bf16x8 part[MT][XT == kF32 ? 3 : 1][4];
+    bf16x8 part[XT == kF32 ? 3 : 1][4];
     if constexpr (XT == kF32) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          split_f32(st.x[mt][2 * i], st.x[mt][2 * i + 1], part[mt][0][i], part[mt][1][i], part[mt][2][i]);
+      for (int i = 0; i < 4; ++i) split_f32(st.x[2 * i], st.x[2 * i + 1], part[0][i], part[1][i], part[2][i]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -225,13 +216,10 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
           const f16x8 w = weights_f16(d[i]);
           // scale byte 0 stands for 2^-127
           const float sc = s[i] ? __uint_as_float(s[i]) : __uint_as_float(0x00400000u);
+          const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, st.x[i]), w,
+                                                               v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, st.x[mt][i]), w,
-                                                                 v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[mt][nt][r] += p[r] * sc;
-          }
+          for (int r = 0; r < 4; ++r) acc[nt][r] += p[r] * sc;
         }
       } else {
         const float sc = __uint_as_float(sbits);
@@ -239,16 +227,12 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bf16x8 w = weights_bf16(d[i], sc);
+          if constexpr (XT == kF32) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (XT == kF32) {
-#pragma unroll
-              for (int h = 2; h >= 0; --h)
-                acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[mt][h][i], w, acc[mt][nt], 0, 0, 0);
-            } else {
-              acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x[mt][i]), w,
-                                                                    acc[mt][nt], 0, 0, 0);
-            }
+            for (int h = 2; h >= 0; --h)
+              acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[h][i], w, acc[nt], 0, 0, 0);
+          } else {
+            acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.x[i]), w, acc[nt], 0, 0, 0);
           }
         }
       }
@@ -256,32 +240,34 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   };
 
   // Steps past K load zeros and add nothing, so the loop has no branch
-  // between a load and its use.
+  // between a load and its use.  The last round loads nothing: out-of-range
+  // loads cost the address unit as much as others (one more round of them made
+  // one row of 4096 x 512 4.2 us instead of 3.5).
   Stage st[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) load(wave + WK * d, st[d]);
   const int rounds = (KS + WK * D - 1) / (WK * D);
-  for (int it = 0; it < rounds; ++it) {
+  for (int it = 0; it + 1 < rounds; ++it) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       compute(wave + WK * (it * D + d), st[d]);
       load(wave + WK * ((it + 1) * D + d), st[d]);
     }
   }
+#pragma unroll
+  for (int d = 0; d < D; ++d) compute(wave + WK * ((rounds - 1) * D + d), st[d]);
 
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (16 * mt + 4 * q4 + r < rows) red[((wave * MT + mt) * NT + nt) * 256 + r * 64 + lane] = acc[mt][nt][r];
+    for (int r = 0; r < 4; ++r)
+      if (4 * q4 + r < rows) red[(wave * NT + nt) * 256 + r * 64 + lane] = acc[nt][r];
   __syncthreads();
   auto sum = [&](int row, int nt, int n) {
-    const int at = ((row >> 4) * NT + nt) * 256 + (row & 3) * 64 + ((row >> 2) & 3) * 16 + n;
+    const int at = nt * 256 + (row & 3) * 64 + (row >> 2) * 16 + n;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WK; ++w) v += red[w * MT * NT * 256 + at];
+    for (int w = 0; w < WK; ++w) v += red[w * NT * 256 + at];
     return v;
   };
   for (int j = threadIdx.x; j < rows * cols; j += 64 * WK) {
@@ -294,20 +280,32 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   }
 }
 
-template <int XT, int MT, int NT, int WK, int D>
+template <int XT, int NT, int WK, int D>
 static hipError_t run_gemv(const GemvArgs &a, hipStream_t stream) {
   const int cols = a.gated ? 8 * NT : 16 * NT;
   const int out_cols = a.gated ? a.N >> 1 : a.N;
-  const dim3 grid((out_cols + cols - 1) / cols, a.ids ? a.M : (a.M + 16 * MT - 1) / (16 * MT));
-  gemv_kernel<XT, MT, NT, WK, D><<<grid, 64 * WK, 0, stream>>>(a);
+  const dim3 grid((out_cols + cols - 1) / cols, a.ids ? a.M : (a.M + 15) / 16);
+  gemv_kernel<XT, NT, WK, D><<<grid, 64 * WK, 0, stream>>>(a);
   return hipGetLastError();
 }
 
+// 16 rows a workgroup whatever M is: reading B again for the next 16, from L2,
+// cost no more than tiles of 32 or 64 rows with their fewer workgroups (256
+// rows of 4096 x 4096, bf16: 23.5 us, 22.5 and 23.7), and less for few rows.
+// Column tiles by how many workgroups they leave: 64 columns where that makes
+// one a CU or more (32 expert rows of 4096 x 2048 24.7 against 26.1 us with 32
+// columns, 64 rows of 7168 x 2048 9.1 against 11.6), 16 where 32 would leave
+// half the CUs idle (13 rows of 2112 x 7168 8.4 against 9.6 us), 32 otherwise
+// (one row of 7168 x 7168 7.0 us; 64 columns 8.5, 16 7.7).  Four waves where
+// that leaves none without a step.  One step a wave and round: two in flight
+// were slower on all of these.
 template <int XT>
 static hipError_t run_gemv_rows(const GemvArgs &a, hipStream_t stream) {
-  if (a.ids || a.M <= 16) return run_gemv<XT, 1, 2, 8, 2>(a, stream);
-  if (a.M <= 32) return run_gemv<XT, 2, 2, 8, 2>(a, stream);
-  return run_gemv<XT, 4, 2, 8, 1>(a, stream);
+  const int64_t row_tiles = a.ids ? a.M : (a.M + 15) / 16;
+  if (row_tiles * (a.N / 64) >= 256) return run_gemv<XT, 4, 4, 1>(a, stream);
+  if (a.gated || row_tiles * (a.N / 32) >= 128)
+    return a.K <= 4 * 128 ? run_gemv<XT, 2, 4, 1>(a, stream) : run_gemv<XT, 2, 8, 1>(a, stream);
+  return run_gemv<XT, 1, 8, 1>(a, stream);
 }
 
 hipError_t launch_gemv(const GemvArgs &a, hipStream_t stream) {
