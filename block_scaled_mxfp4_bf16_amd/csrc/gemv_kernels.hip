@@ -98,7 +98,7 @@ __device__ __forceinline__ void split_f32(const u32x4 &p, const u32x4 &q, bf16x8
 // wave w takes steps w, w + WK, ... with D steps in flight.  With `gated`
 // the first NT/2 subtiles are gate columns and the others their up columns.
 template <int XT, int NT, int WK, int D>
-__global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
+__global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a, int first_tile) {
   constexpr int XL = XT == kF32 ? 8 : 4;  // 16-byte loads of x per step
   constexpr int ES = XT == kF32 ? 4 : 2;  // bytes per element of x
   constexpr int NSD = NT > 1 ? NT : 1;
@@ -112,7 +112,8 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   const int G = K >> 5;
   const int gp = (G + 7) & ~7;
 
-  int row0 = blockIdx.y * 16, rows = a.M - row0;
+  const int row_tile = first_tile + blockIdx.y;
+  int row0 = row_tile * 16, rows = a.M - row0;
   int64_t xrow = row0;
   const uint8_t *Bw = a.Bw, *Bs = a.Bs;
   const int out_cols = a.gated ? N >> 1 : N;
@@ -121,7 +122,7 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   const int s_bytes = ((N + 255) >> 8) * 8 * gp * 32;
   bool live = true;
   if (a.ids) {
-    row0 = blockIdx.y;
+    row0 = row_tile;
     rows = 1;
     xrow = row0 / a.repeat;
     const int id = __builtin_amdgcn_readfirstlane(a.ids[row0]);
@@ -280,12 +281,17 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a) {
   }
 }
 
+constexpr int kMaxGridY = 65535;
+
 template <int XT, int NT, int WK, int D>
 static hipError_t run_gemv(const GemvArgs &a, hipStream_t stream) {
   const int cols = a.gated ? 8 * NT : 16 * NT;
   const int out_cols = a.gated ? a.N >> 1 : a.N;
-  const dim3 grid((out_cols + cols - 1) / cols, a.ids ? a.M : (a.M + 15) / 16);
-  gemv_kernel<XT, NT, WK, D><<<grid, 64 * WK, 0, stream>>>(a);
+  const int tiles = a.ids ? a.M : (a.M + 15) / 16;
+  for (int first = 0; first < tiles; first += kMaxGridY) {
+    const dim3 grid((out_cols + cols - 1) / cols, tiles - first < kMaxGridY ? tiles - first : kMaxGridY);
+    gemv_kernel<XT, NT, WK, D><<<grid, 64 * WK, 0, stream>>>(a, first);
+  }
   return hipGetLastError();
 }
 
