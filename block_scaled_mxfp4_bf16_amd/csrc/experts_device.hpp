@@ -5,6 +5,9 @@
 
 namespace mxfp4 {
 
+template <int V>
+constexpr int kLog2 = V <= 1 ? 0 : 1 + kLog2<V / 2>;
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));

@@ -271,8 +271,9 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a, int fir
     for (int w = 0; w < WK; ++w) v += red[w * NT * 256 + at];
     return v;
   };
-  for (int j = threadIdx.x; j < rows * cols; j += 64 * WK) {
-    const int row = j / cols, c = j - row * cols;
+  const int shift = a.gated ? kLog2<8 * NT> : kLog2<16 * NT>;  // of cols
+  for (int j = threadIdx.x; j < rows << shift; j += 64 * WK) {
+    const int row = j >> shift, c = j - (row << shift);
     const int col = blockIdx.x * cols + c;
     if (col >= out_cols) continue;
     float v = sum(row, c >> 4, c & 15);

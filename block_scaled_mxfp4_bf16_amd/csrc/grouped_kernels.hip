@@ -120,15 +120,30 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a, int
   ((uint32_t *)(a.scales + ((int64_t)(u.tile >> 2) * KS + ks) * 256))[c * 16 + (lane >> 2)] = d;
 }
 
-// Workgroup: 16 * MT rows of one group x 16 * NT columns, all of K; wave w
-// takes steps w, w + WK, ... with D steps in flight.  With `gated` the first
-// NT / 2 subtiles are gate columns and the others their up columns.
-template <int MT, int NT, int WK, int D>
+// Few rows a group, or few columns: 16 rows of one group x 16 * NT columns a
+// workgroup, all of K.  Reading the weights bounds it, so operands go straight
+// to registers and nothing waits at a barrier before the sums; the WK waves
+// take every WK-th K step and add their tiles through LDS in wave order.  With
+// `gated` the first NT / 2 subtiles are gate columns and the others their up
+// columns.  Units of 16 rows also where groups hold more: 64-row units read
+// the weights once instead of up to four times, but from L2 those repeats cost
+// less than the workgroups they spare (771 rows of 16 experts, 2112 x 704: 10.0
+// us with 64 rows, 8.4 with 16).
+template <int NT, int WK>
 __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedArgs a, int n_tiles) {
-  __shared__ __attribute__((aligned(16))) float red[WK * MT * NT * 256];
+  __shared__ __attribute__((aligned(16))) float red[WK * NT * 256];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q4 = lane >> 4;
+  const int N = a.N, K = a.K;
+  const int KS = (K + 127) >> 7;
+  const int gp = ((K >> 5) + 7) & ~7;
+  const int b_bytes = (N >> 4) * K * 8;
+  const int s_bytes = ((N + 255) >> 8) * 8 * gp * 32;
+  const int groups = N >> 4;
+  const int out_cols = a.gated ? N >> 1 : N;
+  const int shift = a.gated ? kLog2<8 * NT> : kLog2<16 * NT>;  // of the columns of a tile
+
   const int64_t work = (int64_t)plan_entry(a, 0).expert * n_tiles;
   for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
     const int index = (int)(item / n_tiles);
@@ -136,28 +151,19 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
     const Unit u = plan_entry(a, 1 + index);
     if (u.expert < 0) continue;
 
-    const int N = a.N, K = a.K;
-    const int KS = (K + 127) >> 7;
-    const int gp = ((K >> 5) + 7) & ~7;
-    const int b_bytes = (N >> 4) * K * 8;
-    const int s_bytes = ((N + 255) >> 8) * 8 * gp * 32;
-    const int rows = u.rows < 16 * MT ? u.rows : 16 * MT;
-    const int tiles = (rows + 15) >> 4;
-    const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(a.codes + (int64_t)u.tile * KS * 1024), 0, tiles * KS * 1024, kRsrcWord3);
+    const int rows = u.rows < 16 ? u.rows : 16;
+    const __amdgpu_buffer_rsrc_t a_rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(a.codes + (int64_t)u.tile * KS * 1024), 0, KS * 1024, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t as_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(a.scales + (int64_t)(u.tile >> 2) * KS * 256), 0, ((MT + 3) / 4) * KS * 256, kRsrcWord3);
+        (void *)(a.scales + (int64_t)(u.tile >> 2) * KS * 256), 0, KS * 256, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t b_rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void *)(a.Bw + (int64_t)u.expert * b_bytes), 0, b_bytes, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t s_rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void *)(a.Bs + (int64_t)u.expert * s_bytes), 0, s_bytes, kRsrcWord3);
-
-    const int groups = N >> 4;
-    const int cols = a.gated ? 8 * NT : 16 * NT;
-    const int first = n_tile * (cols >> 4);
+    const int first = n_tile << (shift - 4);
     int gw[NT];
     bool gok[NT];
-  #pragma unroll
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (a.gated) {
         const int c = first + (nt % (NT / 2));
@@ -168,82 +174,64 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
         gok[nt] = gw[nt] < groups;
       }
     }
-    const int tile_shift = 8 * (u.tile & 3);  // of the first tile's byte in a scale dword (0 unless MT < 4)
+    const int tile_shift = 8 * (u.tile & 3);  // of the rows' byte in a scale dword
 
     struct Stage {
-      u32x4 x[MT];
-      uint32_t xs[(MT + 3) / 4];
+      u32x4 x;
+      uint32_t xs;
       u32x4 b[NT];
       uint32_t s[NT];
-    };
-    auto load = [&](int ks, Stage &st) {
+    } st;
+    auto load = [&](int ks) {
       const bool ok = ks < KS;
-      // a K chunk past the end meets zero rows of A; it is left out of range
-      // only where it would run past the matrix
+      // a K chunk past the end meets zeros of the rows; it must not run past
+      // the matrix all the same
       const bool bk = ok && (4 * ks + q4) * 32 < K;
-  #pragma unroll
+#pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         st.b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
             b_rsrc, off_or_oob(bk && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
         st.s[nt] = __builtin_amdgcn_raw_buffer_load_b32(
             s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
       }
-  #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        st.x[mt] = __builtin_amdgcn_raw_buffer_load_b128(
-            a_rsrc, off_or_oob(ok && mt < tiles, (mt * KS + ks) * 1024 + lane * 16), 0, 0);
-  #pragma unroll
-      for (int q = 0; q < (MT + 3) / 4; ++q)
-        st.xs[q] = __builtin_amdgcn_raw_buffer_load_b32(as_rsrc, off_or_oob(ok, (q * KS + ks) * 256 + lane * 4), 0, 0);
+      st.x = __builtin_amdgcn_raw_buffer_load_b128(a_rsrc, off_or_oob(ok, ks * 1024 + lane * 16), 0, 0);
+      st.xs = __builtin_amdgcn_raw_buffer_load_b32(as_rsrc, off_or_oob(ok, ks * 256 + lane * 4), 0, 0);
     };
-
-    v4f acc[MT][NT];
-  #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-  #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
-    auto compute = [&](int ks, const Stage &st) {
-  #pragma unroll
+    v4f acc[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt] = v4f{0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](int ks) {
+      const uint32_t sa = (st.xs >> tile_shift) & 0xFFu;
+#pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint32_t sb = (st.s[nt] >> (8 * ((gw[nt] & 1) + 2 * (ks & 1)))) & 0xFFu;
-  #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint32_t sa = (st.xs[mt >> 2] >> (tile_shift + 8 * (mt & 3))) & 0xFFu;
-          acc[mt][nt] = mfma_fp4(st.x[mt], st.b[nt], acc[mt][nt], sa, sb);
-        }
+        acc[nt] = mfma_fp4(st.x, st.b[nt], acc[nt], sa, sb);
       }
     };
-
-    Stage st[D];
-  #pragma unroll
-    for (int d = 0; d < D; ++d) load(wave + WK * d, st[d]);
-    const int rounds = (KS + WK * D - 1) / (WK * D);
-    for (int it = 0; it < rounds; ++it) {
-  #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        compute(wave + WK * (it * D + d), st[d]);
-        load(wave + WK * ((it + 1) * D + d), st[d]);
-      }
+    // Steps past K load zeros and add nothing; the last round loads nothing.
+    const int rounds = (KS + WK - 1) / WK;
+    load(wave);
+    for (int it = 0; it + 1 < rounds; ++it) {
+      compute(wave + WK * it);
+      load(wave + WK * (it + 1));
     }
+    compute(wave + WK * (rounds - 1));
 
-  #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-  #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
-        for (int r = 0; r < 4; ++r) red[((wave * MT + mt) * NT + nt) * 256 + r * 64 + lane] = acc[mt][nt][r];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) red[(wave * NT + nt) * 256 + r * 64 + lane] = acc[nt][r];
     __syncthreads();
     auto sum = [&](int row, int nt, int n) {
-      const int at = ((row >> 4) * NT + nt) * 256 + (row & 3) * 64 + ((row >> 2) & 3) * 16 + n;
+      const int at = nt * 256 + (row & 3) * 64 + (row >> 2) * 16 + n;
       float v = 0.f;
-  #pragma unroll
-      for (int w = 0; w < WK; ++w) v += red[w * MT * NT * 256 + at];
+#pragma unroll
+      for (int w = 0; w < WK; ++w) v += red[w * NT * 256 + at];
       return v;
     };
-    const int out_cols = a.gated ? N >> 1 : N;
-    for (int j = threadIdx.x; j < rows * cols; j += 64 * WK) {
-      const int row = j / cols, c = j - row * cols;
-      const int col = n_tile * cols + c;
+    for (int j = threadIdx.x; j < rows << shift; j += 64 * WK) {
+      const int row = j >> shift, c = j - (row << shift);
+      const int col = (n_tile << shift) + c;
       if (col >= out_cols) continue;
       float v = sum(row, c >> 4, c & 15);
       if (a.gated) v = gated_silu(v, sum(row, NT / 2 + (c >> 4), c & 15));
@@ -256,31 +244,43 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
 // Workgroups of a launch (threads of a grid dimension are limited to 2^32).
 constexpr int64_t kMaxGrid = 1 << 22;
 
-template <int MT, int NT, int WK, int D>
 static hipError_t run_stream(const GroupedArgs &a, hipStream_t stream) {
-  const int cols = a.gated ? 8 * NT : 16 * NT;
+  const int cols = a.gated ? 32 : 64;
   const int out_cols = a.gated ? a.N >> 1 : a.N;
   const int n_tiles = (out_cols + cols - 1) / cols;
   const int64_t items = (int64_t)a.max_units * n_tiles;
-  grouped_stream_kernel<MT, NT, WK, D><<<(unsigned)least(items, kMaxGrid), 64 * WK, 0, stream>>>(a, n_tiles);
+  grouped_stream_kernel<4, 4><<<(unsigned)least(items, kMaxGrid), 256, 0, stream>>>(a, n_tiles);
   return hipGetLastError();
 }
+
+static int tile_columns(const GroupedArgs &a) { return a.gated ? (a.N / 2 + 127) / 128 : (a.N + 255) / 256; }
 
 static hipError_t run_tile(const GroupedArgs &a, hipStream_t stream) {
   const int wide = ((uintptr_t)a.C & 15) == 0 && a.ldc % 8 == 0;
   if (a.gated)
-    grouped_tile_kernel<true, 1><<<512, 256, 0, stream>>>(a, (a.N / 2 + 127) / 128, wide);
+    grouped_tile_kernel<true><<<512, 256, 0, stream>>>(a, tile_columns(a), wide);
   else
-    grouped_tile_kernel<false, 1><<<512, 256, 0, stream>>>(a, (a.N + 255) / 256, wide);
+    grouped_tile_kernel<false><<<512, 256, 0, stream>>>(a, tile_columns(a), wide);
   return hipGetLastError();
+}
+
+// Whether the 128-row tiles are the faster form: groups of 32 rows on average
+// and a tile for every CU.  Both timed, 16-row units against tiles: 2048 rows of
+// 64 experts, 2048 x 1024: 18.5 and 16.9 us; 4096 rows, 4096 x 2048: 98 and 72.
+// Below either bound: 1280 rows (20 a group) of 4096 x 1024 31.8 and 34.5; 256
+// rows of 8 experts, 4096 x 2048 (128 tiles) 9.9 and 12.1.  The tiles also need
+// their pairs of column groups whole.
+static bool use_tiles(const GroupedArgs &a) {
+  const int64_t some = least(a.E, a.R);
+  const int64_t units = a.R / 128 > some ? a.R / 128 : some;
+  return a.R / some >= 32 && units * tile_columns(a) >= 256 && a.N % (a.gated ? 64 : 32) == 0;
 }
 
 hipError_t launch_grouped(GroupedArgs a, hipStream_t stream) {
   const int64_t quads = most_units(a.R, a.E, 64), KS = k_steps(a.K);
-  const int64_t mean = a.R / least(a.E, a.R);  // rows of a group, were they even
-  const bool tile = mean > 64 && a.N % (a.gated ? 64 : 32) == 0;
-  a.unit_shift = tile ? 7 : (mean <= 16 ? 4 : 6);
-  a.pairs = tile;
+  const bool tiles = use_tiles(a);
+  a.pairs = tiles;
+  a.unit_shift = tiles ? 7 : 4;
   a.unit_rows = 1 << a.unit_shift;
   a.max_units = (int)most_units(a.R, a.E, a.unit_rows);
   a.quads = (int)quads;
@@ -291,9 +291,7 @@ hipError_t launch_grouped(GroupedArgs a, hipStream_t stream) {
   pack_rows_kernel<<<(unsigned)(quads * runs + 1), 256, 0, stream>>>(a, (int)runs);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (tile) return run_tile(a, stream);
-  if (mean <= 16) return run_stream<1, 2, 8, 2>(a, stream);
-  return run_stream<4, 4, 4, 2>(a, stream);
+  return tiles ? run_tile(a, stream) : run_stream(a, stream);
 }
 
 }  // namespace mxfp4

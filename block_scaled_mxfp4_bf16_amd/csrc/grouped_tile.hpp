@@ -47,10 +47,10 @@ __device__ __forceinline__ v16f mfma32_fp4_sel2(const u32x4 &a, const u32x4 &b, 
   return ia ? mfma32_fp4_at<2>(av, bv, c, sa, sb, ib) : mfma32_fp4_at<0>(av, bv, c, sa, sb, ib);
 }
 
-template <bool GATED, int WM>
-__global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const GroupedArgs a, int n_tiles, int wide_stores) {
-  constexpr int MT = 4;          // 32-row tiles of a wave
-  constexpr int UT = 2 * MT * WM;  // 16-row blocks of a unit
+template <bool GATED>
+__global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs a, int n_tiles, int wide_stores) {
+  constexpr int MT = 4;       // 32-row tiles of a unit
+  constexpr int UT = 2 * MT;  // its 16-row blocks
   constexpr int BN = GATED ? 128 : 256;  // output columns of a tile
   constexpr int STORES = MT * (GATED ? 2 : 4);  // of a wave and tile, 16 bytes a lane
   __shared__ __attribute__((aligned(16))) uint8_t slot0[UT * 1024];
@@ -61,7 +61,6 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
   const int l16 = lane * 16, l4 = lane * 4;
   // The 32x32x64 instruction takes row lane % 32 and K chunk lane / 32 of one
   // half of a step; a 32-row tile is two blocks of 16 rows x 4 chunks.
@@ -107,13 +106,13 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
     const int64_t expert = unit.expert < 0 ? 0 : unit.expert;
     a_size = tiles * KS * 1024;
     as_size = ((tiles + 3) >> 2) * KS * 256;
-    b_size = tiles > 2 * MT * wm ? b_bytes : 0;  // a wave without rows needs no weights
-    s_size = tiles > 2 * MT * wm ? s_bytes : 0;
+    b_size = tiles ? b_bytes : 0;
+    s_size = tiles ? s_bytes : 0;
     a_base = a.codes + (int64_t)unit.tile * KS * 1024;
     as_base = a.scales + (int64_t)(unit.tile >> 2) * KS * 256;
     b_base = a.Bw + expert * b_bytes;
     s_base = a.Bs + expert * s_bytes;
-    col0 = n_tile * BN + wn * (BN / 4);
+    col0 = n_tile * BN + wave * (BN / 4);
     const int g = col0 >> 4;
     const int up = GATED ? N >> 5 : 2;
     const bool ok0 = GATED ? g < (N >> 5) : g < (N >> 4);
@@ -162,14 +161,14 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         st[s].as[q] = __builtin_amdgcn_raw_buffer_load_b32(sized(as_base, ok ? as_size : 0), l4 + s * 256,
-                                                           ((2 * wm + q) * KS + k0) * 256, 0);
+                                                           (q * KS + k0) * 256, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   // Rows 32 mt + lane % 32 of the wave, half h of the step in slot s.
   auto row_block = [&](int s, int i) {
     const int mt = i >> 1, h = i & 1;
-    return *(const u32x4 *)(slot(s) + (wm * 2 * MT + 2 * mt) * 1024 + h * 512 + r1 * 1024 + in_block);
+    return *(const u32x4 *)(slot(s) + 2 * mt * 1024 + h * 512 + r1 * 1024 + in_block);
   };
 
   v16f acc[MT][2];
@@ -182,12 +181,10 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
         for (int i = 0; i < 16; ++i) acc[mt][nt][i] = 0.f;
   };
   auto store = [&](const Unit &u, int col, auto wide) {
-    const int row0 = 32 * MT * wm;
-    const int left = u.expert < 0 ? 0 : u.rows - row0;
-    const int rows = left < 0 ? 0 : (left < 32 * MT ? left : 32 * MT);
+    const int rows = u.expert < 0 ? 0 : (u.rows < 32 * MT ? u.rows : 32 * MT);
     const int ldc = (int)a.ldc * 2;
     const __amdgpu_buffer_rsrc_t c_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(a.C + (int64_t)(u.row + row0) * a.ldc), 0, rows ? (rows - 1) * ldc + out_cols * 2 : 0, kRsrcWord3);
+        (void *)(a.C + (int64_t)u.row * a.ldc), 0, rows ? (rows - 1) * ldc + out_cols * 2 : 0, kRsrcWord3);
     // Element 4 j + r of an accumulator is column 8 j + 4 * (lane / 32) + r of
     // row lane % 32.  A swap of the upper half of the lanes in j = 2 p with the
     // lower half in j = 2 p + 1 leaves each lane eight neighbouring columns,
@@ -260,7 +257,7 @@ __global__ __launch_bounds__(256 * WM, 2) void grouped_tile_kernel(const Grouped
     const bool last = ks + 4 >= steps;  // the last round of this tile
     const Unit tile_unit = unit;
     const int tile_col = col0;
-    const int live = tile_unit.expert < 0 ? 0 : tile_unit.rows - 32 * MT * wm;  // rows of this wave
+    const int live = tile_unit.expert < 0 ? 0 : tile_unit.rows;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // rows(i + 1) have arrived for every wave, and every wave has read
