@@ -29,14 +29,23 @@ struct Unit {
   int row;   // first output row
   int rows;  // output rows from `row` to the end of the group
   int tile;  // its first 16-row tile in the workspace
+  int index; // its number among the expert's units
 };
+
+// An entry's first word holds the expert and, above it, the unit's number
+// among the expert's (at most 2^20 rows of 16 a unit: 17 bits).
+constexpr int kExpertBits = 12, kMaxExperts = 1 << kExpertBits;
 
 // Entries are read through the scalar cache: the index is the same in every
 // lane, and the reads do not queue behind the operand loads.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ Unit plan_entry(const GroupedArgs &a, int i) {
   const i32x4 v = ((const __attribute__((address_space(4))) i32x4 *)a.plan)[i];
-  return Unit{v.x, v.y, v.z, v.w};
+  return Unit{v.x < 0 ? -1 : v.x & (kMaxExperts - 1), v.y, v.z, v.w, v.x >> kExpertBits};
+}
+
+__device__ __forceinline__ int unit_count(const GroupedArgs &a) {
+  return *(const __attribute__((address_space(4))) int *)a.plan;
 }
 
 // Rows of expert e, clamped to [0, R): whatever the offsets hold, no group
@@ -102,7 +111,7 @@ struct GroupScan {
     }
     const int src = __builtin_ctzll(__ballot(expert >= 0) | (1ull << 63));
     return Unit{__builtin_amdgcn_readlane(expert, src), __builtin_amdgcn_readlane(row, src),
-                __builtin_amdgcn_readlane(rows, src), index * 4};
+                __builtin_amdgcn_readlane(rows, src), index * 4, 0};
   }
 
   // Lists the units.  Offsets that do not rise can describe more units and
@@ -113,9 +122,11 @@ struct GroupScan {
       int lo, hi;
       group_range(a, e, lo, hi);
       const int last_quad = q + ((hi - lo + 63) >> 6);
+      int first = e;  // the entry's first word
       for (int row = lo, tile = 4 * q; row < hi; row += a.unit_rows, tile += a.unit_rows >> 4, ++u) {
         const bool fits = last_quad <= a.quads;
-        if (u < a.max_units) a.plan[1 + u] = int4{fits ? e : -1, row, fits ? hi - row : 0, tile};
+        if (u < a.max_units) a.plan[1 + u] = int4{fits ? first : -1, row, fits ? hi - row : 0, tile};
+        first += kMaxExperts;
       }
       q = last_quad;
     }

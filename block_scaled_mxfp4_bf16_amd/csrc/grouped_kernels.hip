@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
   const int out_cols = a.gated ? N >> 1 : N;
   const int shift = a.gated ? kLog2<8 * NT> : kLog2<16 * NT>;  // of the columns of a tile
 
-  const int64_t work = (int64_t)plan_entry(a, 0).expert * n_tiles;
+  const int64_t work = (int64_t)unit_count(a) * n_tiles;
   for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
     const int index = (int)(item / n_tiles);
     const int n_tile = (int)(item - (int64_t)index * n_tiles);

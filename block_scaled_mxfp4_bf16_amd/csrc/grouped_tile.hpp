@@ -47,6 +47,13 @@ __device__ __forceinline__ v16f mfma32_fp4_sel2(const u32x4 &a, const u32x4 &b, 
   return ia ? mfma32_fp4_at<2>(av, bv, c, sa, sb, ib) : mfma32_fp4_at<0>(av, bv, c, sa, sb, ib);
 }
 
+// The units of an expert are taken in blocks of up to kBlockUnits, the unit
+// fastest within a block, so that the workgroups of an XCD that read the same
+// weights do it at the same time and the second reader finds them in L2.
+// Column tiles fastest instead made 32768 rows of 64 experts, 4096 x 2048 gated,
+// read 865 MB through L2 where this reads 400 (199 against 193 us a call).
+constexpr int kBlockUnits = 8;
+
 template <bool GATED>
 __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs a, int n_tiles, int wide_stores) {
   constexpr int MT = 4;       // 32-row tiles of a unit
@@ -75,9 +82,8 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
   const int out_cols = GATED ? N >> 1 : N;
 
   // Workgroup b runs on XCD b % 8.  Each XCD takes a contiguous range of the
-  // items (unit, n tile), n tile fastest, so that an expert's weights and
-  // rows stay in one L2.
-  const int units = plan_entry(a, 0).expert;
+  // items (unit, n tile), so that an expert's weights and rows stay in one L2.
+  const int units = unit_count(a);
   const int items = units * n_tiles;
   const int xcd = blockIdx.x & 7;
   const int stride = gridDim.x >> 3;
@@ -98,10 +104,21 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
 
   auto enter = [&]() {
     none = next_item >= end;
-    const int u = none ? 0 : next_item / n_tiles;
-    const int n_tile = none ? 0 : next_item - u * n_tiles;
-    next_item += stride;
+    int u = none ? 0 : next_item / n_tiles, n_tile = 0;
     unit = plan_entry(a, 1 + u);
+    if (!none && unit.expert >= 0) {
+      const int first = u - unit.index;
+      const int all = unit.index + ((unit.rows + 16 * UT - 1) / (16 * UT));
+      const int in_expert = next_item - first * n_tiles;
+      const int block = in_expert / (kBlockUnits * n_tiles);
+      const int in_block = in_expert - block * kBlockUnits * n_tiles;
+      const int listed = all < units - first ? all : units - first;
+      const int width = listed - kBlockUnits * block < kBlockUnits ? listed - kBlockUnits * block : kBlockUnits;
+      n_tile = in_block / width;
+      u = first + kBlockUnits * block + in_block - n_tile * width;
+      unit = plan_entry(a, 1 + u);
+    }
+    next_item += stride;
     const int tiles = none || unit.expert < 0 ? 0 : (unit.rows < 16 * UT ? (unit.rows + 15) >> 4 : UT);
     const int64_t expert = unit.expert < 0 ? 0 : unit.expert;
     a_size = tiles * KS * 1024;
