@@ -110,6 +110,7 @@ def _ptr(x):
 
 
 _raw_stream = None
+_current_device = None
 
 
 def _current_stream():
@@ -383,8 +384,15 @@ def _prepared(Bw, Bs, N, K, dev):
 
 
 def _on_gpu(dev):
+    """A launch goes to the current device; tensors of another would be read from there."""
+    global _current_device
     if dev < 0:
         raise ValueError("the expert operators take cuda tensors")
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if dev != _current_device():
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (dev, _current_device()))
 
 
 def prepare_experts(B, stream=None):
