@@ -126,14 +126,14 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
   if constexpr (BIAS) {
     float g[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) g[v] = softmax ? __expf(x[v] - top) : 1.0f / (1.0f + __expf(-x[v]));
+    for (int v = 0; v < V; ++v) g[v] = softmax ? __expf(x[v] - top) : __builtin_amdgcn_rcpf(1.0f + __expf(-x[v]));
     float scale = 1.f;
     if (softmax) {
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) s += g[v];
       s = all_reduce<L>(s, plus);
-      scale = s > 0.f ? 1.0f / s : 0.f;
+      scale = s > 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -152,32 +152,31 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
 #pragma unroll
     for (int v = 1; v < V; ++v) m = larger(m, key[v]);
     m = all_reduce<L>(m, larger);
-    uint32_t near = m;  // keys from here on may be the largest
+    int c = INT32_MAX;
     if constexpr (BIAS) {
       const float top_value = value_of(m ? m : 0x80000000u);
-      near = order_of(top_value - (0x1p-18f + 0x1p-22f * __builtin_fabsf(top_value)));
-      near = m ? (near ? near : 1u) : 0u;
-    }
-    int c = INT32_MAX, c_last = -1;
+      const uint32_t below = order_of(top_value - (0x1p-18f + 0x1p-22f * __builtin_fabsf(top_value)));
+      const uint32_t near = m && below ? below : 1u;  // keys from here on may be the largest
+      int n = 0;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) {
-      const bool is = key[v] >= near;
-      c = is ? l + L * v : c;
-      if constexpr (BIAS) c_last = is ? larger(c_last, l + L * v) : c_last;
-    }
-    c = all_reduce<L>(c, smaller);
-    if constexpr (BIAS) {
-      c_last = all_reduce<L>(c_last, larger);
-      if (__ballot(m && c != c_last)) {
+      for (int v = V - 1; v >= 0; --v) {
+        const bool is = key[v] >= near;
+        n += is;
+        c = is ? l + L * v : c;
+      }
+      const uint64_t with = __ballot(n != 0) >> (__lane_id() & (64 - L));
+      const int lanes = __builtin_popcountll(L == 64 ? with : with & ((1ull << (L & 63)) - 1));
+      c = all_reduce<L>(c, smaller);
+      if (__ballot(n > 1 || lanes > 1)) {
         // more than one candidate in some token of the wave: decide by f64
         if (softmax && sum_all == 0.0) sum_all = sum64();
         uint64_t best = 0;
         int at = INT32_MAX;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (__ballot(m && key[v] >= near)) {
+          if (__ballot(key[v] >= near)) {
             const double g = softmax ? exp((double)x[v] - top) / sum_all : 1.0 / (1.0 + exp(-(double)x[v]));
-            const uint64_t o = m && key[v] >= near ? order_of(g + bias[v]) : 0;
+            const uint64_t o = key[v] >= near ? order_of(g + bias[v]) : 0;
             at = o > best ? l + L * v : at;
             best = larger(best, o);
           }
@@ -185,11 +184,21 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
         const uint64_t all = all_reduce<L>(best, larger);
         const int exact = all_reduce<L>(best == all ? at : INT32_MAX, smaller);
         c = m ? exact : c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = l + L * v == c ? 0 : key[v];
+      } else {
+        // the one candidate of each token
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] >= near ? 0 : key[v];
       }
+    } else {
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v) c = key[v] == m ? l + L * v : c;
+      c = all_reduce<L>(c, smaller);
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = l + L * v == c ? 0 : key[v];
     }
     if (l == j) id = m ? c : -1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = l + L * v == c ? 0 : key[v];
   }
 
   double w = 0.0;
