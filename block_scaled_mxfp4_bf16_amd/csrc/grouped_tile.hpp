@@ -60,10 +60,12 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
   constexpr int UT = 2 * MT;  // its 16-row blocks
   constexpr int BN = GATED ? 128 : 256;  // output columns of a tile
   constexpr int STORES = MT * (GATED ? 2 : 4);  // of a wave and tile, 16 bytes a lane
+  constexpr int CHUNKS = GATED ? 4 : 8;  // of 8 columns, of a wave
   __shared__ __attribute__((aligned(16))) uint8_t slot0[UT * 1024];
   __shared__ __attribute__((aligned(16))) uint8_t slot1[UT * 1024];
   __shared__ __attribute__((aligned(16))) uint8_t slot2[UT * 1024];
   __shared__ __attribute__((aligned(16))) uint8_t slot3[UT * 1024];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[4 * 32 * CHUNKS * 16];
   const auto slot = [&](int s) -> uint8_t * { return s == 0 ? slot0 : (s == 1 ? slot1 : (s == 2 ? slot2 : slot3)); };
 
   const int lane = threadIdx.x & 63;
@@ -204,50 +206,62 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
         (void *)(a.C + (int64_t)u.row * a.ldc), 0, rows ? (rows - 1) * ldc + out_cols * 2 : 0, kRsrcWord3);
     // Element 4 j + r of an accumulator is column 8 j + 4 * (lane / 32) + r of
     // row lane % 32.  A swap of the upper half of the lanes in j = 2 p with the
-    // lower half in j = 2 p + 1 leaves each lane eight neighbouring columns,
-    // one 16-byte store.
+    // lower half in j = 2 p + 1 leaves each lane eight neighbouring columns, 16
+    // bytes.  Stored as they lie, two lanes of a row would write 32 bytes of
+    // it; through LDS, 32 rows at a time, a store covers all of the wave's
+    // columns of a row (32768 rows of 64 experts, 2048 x 2048: 102 us without,
+    // 91 with it; 4096 x 2048 gated, half the columns: 169 and 166).
     // The lane number is found anew for each tile, from a zero that the
     // compiler cannot see through: it would keep the offsets of every store
     // through the products otherwise, and has no registers for them.
     uint32_t zero = 0;
     asm volatile("" : "+s"(zero));
     const int me = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
-    const int at = (me & 31) * ldc + (col + 8 * (me >> 5)) * 2;
+    uint8_t *const turn = turned + wave * 32 * CHUNKS * 16;
+    const auto place = [&](int row, int chunk) {  // of a chunk of 8 columns; no two rows of a group in the same banks
+      return (u32x4 *)(turn + (row * CHUNKS + (chunk ^ ((CHUNKS == 8 ? row : row >> 1) & (CHUNKS - 1)))) * 16);
+    };
+    const int chunk = me & (CHUNKS - 1), first_row = me / CHUNKS;
+    const int at = first_row * ldc + (col + 8 * chunk) * 2;
+    const bool col_ok = col + 8 * chunk < out_cols;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const bool row_ok = 32 * mt + (me & 31) < rows;
 #pragma unroll
-      for (int nt = 0; nt < (GATED ? 1 : 2); ++nt) {
+      for (int part = 0; part < CHUNKS / 2; ++part) {
+        const int nt = part >> 1, p = part & 1;
+        uint32_t d[2][2];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t d[2][2];
+        for (int j = 0; j < 2; ++j) {
+          float v[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int i = 8 * p + 4 * j + r;
-              v[r] = GATED ? gated_silu(acc[mt][0][i], acc[mt][1][i]) : acc[mt][nt][i];
-            }
-            d[j][0] = bf16x2_rne(v[0], v[1]);
-            d[j][1] = bf16x2_rne(v[2], v[3]);
+          for (int r = 0; r < 4; ++r) {
+            const int i = 8 * p + 4 * j + r;
+            v[r] = GATED ? gated_silu(acc[mt][0][i], acc[mt][1][i]) : acc[mt][nt][i];
           }
-          swap32(d[0][0], d[1][0]);
-          swap32(d[0][1], d[1][1]);
-          const int off = off_or_oob(row_ok && col + 32 * nt < out_cols, at + 32 * mt * ldc + 64 * nt + 32 * p);
-          if constexpr (decltype(wide)::value) {
-            __builtin_amdgcn_raw_buffer_store_b128(u32x4{d[0][0], d[0][1], d[1][0], d[1][1]}, c_rsrc, off, 0, 0);
-          } else {
+          d[j][0] = bf16x2_rne(v[0], v[1]);
+          d[j][1] = bf16x2_rne(v[2], v[3]);
+        }
+        swap32(d[0][0], d[1][0]);
+        swap32(d[0][1], d[1][1]);
+        *place(me & 31, 2 * part + (me >> 5)) = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
+        __builtin_amdgcn_sched_barrier(0);  // few values at a time: the registers are full
+      }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w = d[i >> 1][i & 1];
-              __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, c_rsrc, off, 4 * i, 0);
-              __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> 16), c_rsrc, off, 4 * i + 2, 0);
-            }
+      for (int s = 0; s < CHUNKS / 2; ++s) {
+        const int row = s * (64 / CHUNKS) + first_row;
+        const u32x4 d = *place(row, chunk);
+        const int off = off_or_oob(col_ok && 32 * mt + row < rows, at + (32 * mt + s * (64 / CHUNKS)) * ldc);
+        if constexpr (decltype(wide)::value) {
+          __builtin_amdgcn_raw_buffer_store_b128(d, c_rsrc, off, 0, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)d[i], c_rsrc, off, 4 * i, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(d[i] >> 16), c_rsrc, off, 4 * i + 2, 0);
           }
-          __builtin_amdgcn_sched_barrier(0);  // few values at a time: the registers are full
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
