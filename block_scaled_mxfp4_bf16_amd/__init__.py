@@ -332,22 +332,42 @@ def gemm(A, Bw, Bs, N: int, out=None, stream=None):
 
 MXFP4_TYPE_BF16, MXFP4_TYPE_F16, MXFP4_TYPE_F32 = 0, 1, 2
 
+_torch = None
 _types = {}
+
+
+def _start():
+    """torch and the library, once."""
+    global _torch
+    L = _load()
+    import torch
+    _types.update({torch.bfloat16: MXFP4_TYPE_BF16, torch.float16: MXFP4_TYPE_F16, torch.float32: MXFP4_TYPE_F32})
+    _torch = torch
+    return L
 
 
 def _type(t):
     """MXFP4_TYPE_* of a tensor's dtype."""
-    if not _types:
-        import torch
-        _types.update({torch.bfloat16: MXFP4_TYPE_BF16, torch.float16: MXFP4_TYPE_F16, torch.float32: MXFP4_TYPE_F32})
     r = _types.get(t.dtype)
     if r is None:
         raise TypeError("expected a bf16, f16 or f32 tensor, got %s" % t.dtype)
     return r
 
 
+def _matrix(t, what, names):
+    """Rows, columns, row stride and device of a matrix whose rows are contiguous."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be [%s]" % (what, names))
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s must be a [%s] tensor with contiguous rows" % (what, names))
+    return rows, cols, ld if rows > 1 else cols, t.get_device()
+
+
 def _array(t, dtype, what, n, dev):
-    if t.dtype != dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (what, dtype, n, _device(dev)))
 
 
@@ -356,14 +376,14 @@ def _device(dev):
 
 
 def _rows_of(t, what, rows, cols, dev):
-    """Row stride of a [rows, cols] tensor whose rows are contiguous; rows may be None."""
+    """Row stride of a [rows, cols] tensor whose rows are contiguous."""
     shape = t.shape
-    if len(shape) == 2 and (rows is None or shape[0] == rows) and shape[1] == cols and t.get_device() == dev:
+    if len(shape) == 2 and shape[0] == rows and shape[1] == cols and t.get_device() == dev:
         ld, step = t.stride()
         if step == 1 or cols <= 1:
             return ld if shape[0] > 1 else cols
-    raise ValueError("%s must be a [%s, %d] tensor on %s with contiguous rows" %
-                     (what, "rows" if rows is None else rows, cols, _device(dev)))
+    raise ValueError("%s must be a [%d, %d] tensor on %s with contiguous rows" %
+                     (what, rows, cols, _device(dev)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -374,9 +394,9 @@ def _prepared_bytes(N, K):
 def _prepared(Bw, Bs, N, K, dev):
     """Number of matrices in prepared codes and scales; checks their sizes."""
     per_w, per_s = _prepared_bytes(N, K)
-    total = Bw.numel()
+    total = Bw.nbytes
     E = total // per_w if per_w else 0
-    if E < 1 or total != E * per_w or Bs.numel() != E * per_s or Bw.itemsize != 1 or Bs.itemsize != 1 \
+    if E < 1 or total != E * per_w or Bs.nbytes != E * per_s \
             or not Bw.is_contiguous() or not Bs.is_contiguous() or Bw.get_device() != dev or Bs.get_device() != dev:
         raise ValueError("Bw and Bs must be contiguous byte tensors of prepared [%d, %d] matrices on %s" %
                          (N, K, _device(dev)))
@@ -416,12 +436,9 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
     of y takes matrix ids[r] and row r // repeat of x, and a row whose id is
     none of them is zero.  gated: N/2 columns, silu(first half) * second.
     y's type is out's, else out_dtype, else x's."""
-    import torch
-    if x.dim() != 2:
-        raise ValueError("x must be [M, K]")
-    tokens, K = x.shape
-    dev = x.get_device()
-    ldx = _rows_of(x, "x", None, K, dev)
+    L = _lib if _torch else _start()
+    torch = _torch
+    tokens, K, ldx, dev = _matrix(x, "x", "M, K")
     xt = _type(x)
     E = _prepared(Bw, Bs, N, K, dev)
     M = tokens * repeat
@@ -439,7 +456,7 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
     yt = _type(out)
     _on_gpu(dev)
     if M:
-        rc = _load().mxfp4_gemv(x.data_ptr(), xt, ldx, Bw.data_ptr(), Bs.data_ptr(), ids, E, out.data_ptr(), yt, ldy, M, N,
+        rc = L.mxfp4_gemv(x.data_ptr(), xt, ldx, Bw.data_ptr(), Bs.data_ptr(), ids, E, out.data_ptr(), yt, ldy, M, N,
                                 K, repeat, 1 if gated else 0, _current_stream() if stream is None else _stream(stream))
         if rc:
             _check(rc, "mxfp4_gemv")
@@ -453,12 +470,9 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
     prepare_experts; offsets int32 [E + 1].  row(p) is rows[p] // repeat (int32
     [R], from moe_route with repeat = k), or p without rows.  gated: N/2
     columns, silu(first half) * second.  Rows of no group are zero."""
-    import torch
-    if A.dim() != 2:
-        raise ValueError("A must be [rows, K]")
-    T, K = A.shape
-    dev = A.get_device()
-    lda = _rows_of(A, "A", T, K, dev)
+    L = _lib if _torch else _start()
+    torch = _torch
+    T, K, lda, dev = _matrix(A, "A", "rows, K")
     if A.dtype != torch.bfloat16:
         raise TypeError("A must be bf16, not %s" % A.dtype)
     E = _prepared(Bw, Bs, N, K, dev)
@@ -478,7 +492,7 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
         if out.dtype != torch.bfloat16:
             raise TypeError("out must be bf16, not %s" % out.dtype)
     _on_gpu(dev)
-    rc = _load().mxfp4_gemm_grouped(A.data_ptr(), lda, T, Bw.data_ptr(), Bs.data_ptr(), E, offsets.data_ptr(), rows, repeat,
+    rc = L.mxfp4_gemm_grouped(A.data_ptr(), lda, T, Bw.data_ptr(), Bs.data_ptr(), E, offsets.data_ptr(), rows, repeat,
                                     out.data_ptr(), ldc, R, N, K, 1 if gated else 0, None, 0,
                                     _current_stream() if stream is None else _stream(stream))
     if rc:
@@ -501,12 +515,9 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
       offsets int32 [E + 1], where each expert's pairs lie in rows
       rows    int32 [T * k], the pair t * k + j at each sorted place, or -1
       pos     int32 [T, k], the sorted place of each pair, or -1"""
-    import torch
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
-    T, E = logits.shape
-    dev = logits.get_device()
-    ld = _rows_of(logits, "logits", T, E, dev)
+    L = _lib if _torch else _start()
+    torch = _torch
+    T, E, ld, dev = _matrix(logits, "logits", "T, E")
     lt = _type(logits)
     kind = _scores.get(score)
     if kind is None:
@@ -528,7 +539,7 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
         _array(rows, torch.int32, "rows", n, dev)
         _array(pos, torch.int32, "pos", n, dev)
     _on_gpu(dev)
-    rc = _load().mxfp4_moe_route(logits.data_ptr(), lt, ld, bias, T, E, k, kind, 1 if renormalize else 0, ids.data_ptr(),
+    rc = L.mxfp4_moe_route(logits.data_ptr(), lt, ld, bias, T, E, k, kind, 1 if renormalize else 0, ids.data_ptr(),
                                  weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), None, 0,
                                  _current_stream() if stream is None else _stream(stream))
     if rc:
@@ -543,13 +554,12 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
     int32 [T, k] (row t * k + j without it; a place outside y adds nothing);
     residual [T, N] of out's type, which may be out itself.  out's type is
     out's, else out_dtype, else residual's, else bf16."""
-    import torch
-    if y.dim() != 2 or weights.dim() != 2:
-        raise ValueError("y must be [rows, N] and weights [T, k]")
-    R, N = y.shape
+    L = _lib if _torch else _start()
+    torch = _torch
+    R, N, ld_y, dev = _matrix(y, "y", "rows, N")
+    if weights.dim() != 2:
+        raise ValueError("weights must be [T, k]")
     T, k = weights.shape
-    dev = y.get_device()
-    ld_y = _rows_of(y, "y", R, N, dev)
     yt = _type(y)
     _array(weights, torch.float32, "weights", T * k, dev)
     if pos is not None:
@@ -571,7 +581,7 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
         residual = residual.data_ptr()
     ot = _type(out)
     _on_gpu(dev)
-    rc = _load().mxfp4_moe_combine(y.data_ptr(), yt, ld_y, R, weights.data_ptr(), pos, residual, ld_res, out.data_ptr(), ot,
+    rc = L.mxfp4_moe_combine(y.data_ptr(), yt, ld_y, R, weights.data_ptr(), pos, residual, ld_res, out.data_ptr(), ot,
                                    ld_out, T, k, N, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_moe_combine")
