@@ -32,6 +32,9 @@ size_t grouped_workspace_bytes(int64_t R, int64_t K, int64_t E) {
   return (size_t)(plan_bytes(R, E) + most_units(R, E, 64) * k_steps(K) * (4096 + 256));
 }
 
+// Cache policy of a buffer load: the line is the first to go.
+constexpr int kNonTemporal = 2;
+
 // Gather and quantize.  One wave takes one K step of a quad, the four waves of
 // a workgroup four consecutive ones, and workgroups next to each other the
 // steps of one quad, so that rows are read in long runs.  Four lanes share a
@@ -129,10 +132,12 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a, int
 // columns.  Units of 16 rows also where groups hold more: 64-row units read
 // the weights once instead of up to four times, but from L2 those repeats cost
 // less than the workgroups they spare (771 rows of 16 experts, 2112 x 704: 10.0
-// us with 64 rows, 8.4 with 16).  256 rows of 64 experts, 4096 x 2048: 46.7 us, 6.0
-// TB/s of weights; 32 columns or 8 waves instead: 48.9 and 46.4, but 17.2 and 17.5
-// for 15.2 of 700 rows of 32 experts, 4096 x 1024.
-template <int NT, int WK>
+// us with 64 rows, 8.4 with 16).  256 rows of 64 experts, 4096 x 2048: 45.0 us, 6.2
+// TB/s of weights; 32 columns or 8 waves instead (weights through the caches, then
+// 46.8): 48.9 and 46.4, but 17.2 and 17.5 for 15.2 of 700 rows of 32 experts, 4096 x
+// 1024.
+// ONCE: weights that no cache will hold until they are read again go past them.
+template <int NT, int WK, bool ONCE>
 __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedArgs a, int n_tiles) {
   __shared__ __attribute__((aligned(16))) float red[WK * NT * 256];
   const int lane = threadIdx.x & 63;
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         st.b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
-            b_rsrc, off_or_oob(bk && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
+            b_rsrc, off_or_oob(bk && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, ONCE ? kNonTemporal : 0);
         st.s[nt] = __builtin_amdgcn_raw_buffer_load_b32(
             s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
       }
@@ -247,12 +252,26 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
 // Workgroups of a launch (threads of a grid dimension are limited to 2^32).
 constexpr int64_t kMaxGrid = 1 << 22;
 
+// Whether the weights are read once: 8 rows a group at most on average, so that
+// few groups have a second unit, and 96 MiB of them or more, which the caches do not
+// keep between calls beside everything else.  4096 x 2048 gated, through the
+// caches and past them: 64 experts (285 MB), 1 row a group on average 33.4 and
+// 31.0 us, 4 rows 47.1 and 45.0, 8 rows 50.5 and 48.1, 16 rows 57.8 and 61.2; 16
+// experts (71 MB) 13.6 and 13.8.
+static bool read_once(const GroupedArgs &a) {
+  return a.R / least(a.E, a.R) <= 8 && (int64_t)a.E * a.N * (a.K / 2) >= (int64_t)96 << 20;
+}
+
 static hipError_t run_stream(const GroupedArgs &a, hipStream_t stream) {
   const int cols = a.gated ? 32 : 64;
   const int out_cols = a.gated ? a.N >> 1 : a.N;
   const int n_tiles = (out_cols + cols - 1) / cols;
   const int64_t items = (int64_t)a.max_units * n_tiles;
-  grouped_stream_kernel<4, 4><<<(unsigned)least(items, kMaxGrid), 256, 0, stream>>>(a, n_tiles);
+  const unsigned grid = (unsigned)least(items, kMaxGrid);
+  if (read_once(a))
+    grouped_stream_kernel<4, 4, true><<<grid, 256, 0, stream>>>(a, n_tiles);
+  else
+    grouped_stream_kernel<4, 4, false><<<grid, 256, 0, stream>>>(a, n_tiles);
   return hipGetLastError();
 }
 
