@@ -28,14 +28,15 @@ inline bool matrix_fits(int64_t N, int64_t K) {
 }
 
 // The caller's workspace if it gave one, else the library's, behind the
-// ticket words that the split-K products keep at zero.
-mxfp4_status_t take_workspace(void *given, size_t given_bytes, size_t need, hipStream_t stream, void **out) {
+// ticket words that the split-K products keep at zero; `held` keeps that one
+// for this call while it lives.
+mxfp4_status_t take_workspace(void *given, size_t given_bytes, size_t need, hipStream_t stream, HeldWorkspace *held,
+                              void **out) {
   *out = given;
   if (given) return given_bytes >= need && aligned(given, 256) ? MXFP4_OK : MXFP4_ERR_WORKSPACE;
   if (need == 0) return MXFP4_OK;
-  void *p = nullptr;
-  const mxfp4_status_t st = get_workspace(kTicketBytes + need, stream, &p);
-  if (st == MXFP4_OK) *out = (char *)p + kTicketBytes;
+  const mxfp4_status_t st = hold_workspace(kTicketBytes + need, stream, held);
+  if (st == MXFP4_OK) *out = (char *)held->ptr + kTicketBytes;
   return st;
 }
 
@@ -45,8 +46,7 @@ extern "C" {
 
 mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream) {
   if (bytes > ((size_t)1 << 46)) return MXFP4_ERR_UNSUPPORTED;
-  void *p = nullptr;
-  return get_workspace(bytes ? kTicketBytes + bytes : 0, (hipStream_t)stream, &p);
+  return ready_workspace(bytes ? kTicketBytes + bytes : 0, (hipStream_t)stream);
 }
 
 size_t mxfp4_moe_route_workspace_bytes(int64_t T, int64_t E) {
@@ -65,9 +65,10 @@ mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const
     return MXFP4_ERR_INVALID_ARG;
   if (T > kMaxRows || E > kRouteMaxExperts || k > kRouteMaxChoices || ld > ((int64_t)1 << 40))
     return MXFP4_ERR_UNSUPPORTED;
+  HeldWorkspace held;
   void *ws = nullptr;
   const mxfp4_status_t st =
-      take_workspace(workspace, workspace_bytes, route_workspace_bytes(T, E), (hipStream_t)stream, &ws);
+      take_workspace(workspace, workspace_bytes, route_workspace_bytes(T, E), (hipStream_t)stream, &held, &ws);
   if (st != MXFP4_OK) return st;
   RouteArgs a{};
   a.logits = logits;
@@ -108,9 +109,10 @@ mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, co
       !aligned(rows, 4) || !aligned(C, 2))
     return MXFP4_ERR_INVALID_ARG;
   if (R == 0) return MXFP4_OK;
+  HeldWorkspace held;
   void *ws = nullptr;
   const mxfp4_status_t st = take_workspace(workspace, workspace_bytes, grouped_workspace_bytes(R, K, experts),
-                                           (hipStream_t)stream, &ws);
+                                           (hipStream_t)stream, &held, &ws);
   if (st != MXFP4_OK) return st;
   GroupedArgs a{};
   a.A = (const uint16_t *)A;

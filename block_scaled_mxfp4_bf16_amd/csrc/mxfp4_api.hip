@@ -13,7 +13,6 @@
 
 #include "../../include/mxfp4.h"
 #include "mxfp4_internal.hpp"
-#include "workspace_pool.hpp"
 
 using namespace mxfp4;
 
@@ -363,18 +362,25 @@ int alloc_workspace(int device, void *stream, size_t bytes, void **out) {
   return MXFP4_OK;
 }
 
-WorkspacePool<int (*)(int, void *, size_t, void **)> g_ws(alloc_workspace);
+Workspaces g_ws(alloc_workspace);
 
 }  // namespace
 
 namespace mxfp4 {
 
-mxfp4_status_t get_workspace(size_t need, hipStream_t stream, void **out) {
-  *out = nullptr;
+mxfp4_status_t ready_workspace(size_t need, hipStream_t stream) {
   if (need == 0) return MXFP4_OK;
   int dev = 0;
   if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
-  return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, out);
+  void *p = nullptr;
+  return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, &p);
+}
+
+mxfp4_status_t hold_workspace(size_t need, hipStream_t stream, HeldWorkspace *out) {
+  if (need == 0) return MXFP4_OK;
+  int dev = 0;
+  if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
+  return (mxfp4_status_t)g_ws.hold(dev, (void *)stream, need, &out->ptr, &out->lock);
 }
 
 }  // namespace mxfp4
@@ -537,10 +543,10 @@ mxfp4_status_t mxfp4_gemm(const void *A, const void *Bq_sh, const void *Bs_sh, v
   Schedule s;
   if (!choose((int)M, (int)N, (int)K, &s)) return MXFP4_ERR_UNSUPPORTED;
   const size_t need = gemm_workspace_bytes(s, (int)M, (int)N, (int)K);
-  void *ws = nullptr;
-  st = get_workspace(need, (hipStream_t)stream, &ws);
+  HeldWorkspace ws;
+  st = hold_workspace(need, (hipStream_t)stream, &ws);
   if (st != MXFP4_OK) return st;
-  GemmArgs a{A, Bq_sh, Bs_sh, C, ws, (int)M, (int)N, (int)K};
+  GemmArgs a{A, Bq_sh, Bs_sh, C, ws.ptr, (int)M, (int)N, (int)K};
   return hip_status(launch_gemm(s, a, sw_quant(), (hipStream_t)stream));
 }
 
@@ -569,10 +575,10 @@ mxfp4_status_t mxfp4_gemm_q(const void *Aq, const void *As_shuffled, const void 
   if (pad_to(M, 256) * pad_to(K / 32, 8) >= kMaxBytes) return MXFP4_ERR_UNSUPPORTED;
   Schedule s;
   if (!choose((int)M, (int)N, (int)K, &s, true)) return MXFP4_ERR_UNSUPPORTED;
-  void *ws = nullptr;
-  st = get_workspace(gemm_workspace_bytes(s, (int)M, (int)N, (int)K), (hipStream_t)stream, &ws);
+  HeldWorkspace ws;
+  st = hold_workspace(gemm_workspace_bytes(s, (int)M, (int)N, (int)K), (hipStream_t)stream, &ws);
   if (st != MXFP4_OK) return st;
-  GemmArgs a{nullptr, Bq_sh, Bs_sh, C, ws, (int)M, (int)N, (int)K};
+  GemmArgs a{nullptr, Bq_sh, Bs_sh, C, ws.ptr, (int)M, (int)N, (int)K};
   a.Aq = Aq;
   a.As = As_shuffled;
   return hip_status(launch_gemm(s, a, false, (hipStream_t)stream));
@@ -629,8 +635,7 @@ mxfp4_status_t mxfp4_reserve(int64_t M, int64_t N, int64_t K, mxfp4_stream_t str
   if (K % 64 != 0 || N % 32 != 0) return MXFP4_ERR_UNSUPPORTED;
   Schedule s;
   if (!choose((int)M, (int)N, (int)K, &s)) return MXFP4_ERR_UNSUPPORTED;
-  void *ws = nullptr;
-  return get_workspace(gemm_workspace_bytes(s, (int)M, (int)N, (int)K), (hipStream_t)stream, &ws);
+  return ready_workspace(gemm_workspace_bytes(s, (int)M, (int)N, (int)K), (hipStream_t)stream);
 }
 
 }  // extern "C"

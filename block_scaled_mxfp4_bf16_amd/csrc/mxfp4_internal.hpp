@@ -6,14 +6,24 @@
 #include <stdint.h>
 
 #include "../../include/mxfp4.h"
+#include "workspace_pool.hpp"
 
 namespace mxfp4 {
 
+// The library-owned workspace of (current device, stream), kept from other
+// calls while this lives: a call keeps it until its last launch is enqueued.
+typedef WorkspacePool<int (*)(int, void *, size_t, void **)> Workspaces;
+struct HeldWorkspace {
+  void *ptr = nullptr;
+  Workspaces::Lock lock;
+};
+
 // Shared by the files that hold entry points (mxfp4_api.hip): the status of
-// a HIP call, the library-owned workspace of (current device, stream), and
-// the encoder mode.
+// a HIP call, the library-owned workspaces (only made ready, or held for a
+// call), and the encoder mode.
 mxfp4_status_t hip_status(hipError_t e);
-mxfp4_status_t get_workspace(size_t need, hipStream_t stream, void **out);
+mxfp4_status_t ready_workspace(size_t need, hipStream_t stream);
+mxfp4_status_t hold_workspace(size_t need, hipStream_t stream, HeldWorkspace *out);
 bool sw_quant();
 
 // A GEMM schedule: compile-time tile shape plus the runtime split count.

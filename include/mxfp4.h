@@ -175,6 +175,8 @@ MXFP4_API const char *mxfp4_gemm_q_schedule_name(int64_t M, int64_t N, int64_t K
 /* stays allocated until the process ends, so a HIP graph captured before    */
 /* the growth still replays into valid memory (growth at least doubles the   */
 /* size, so what stays behind is at most about the live buffer's size).      */
+/* A call keeps the workspace to itself until its last launch is enqueued, so */
+/* host threads may call on one stream at once; a second one waits.          */
 /* The device is the calling thread's current device, which `stream` must    */
 /* belong to.  Results are deterministic: the split-K partial sums */
 /* are added in a fixed order (unless an "_at" schedule is forced by         */
@@ -195,7 +197,7 @@ MXFP4_API mxfp4_status_t mxfp4_gemm(const void *A, const void *Bq_sh, const void
  * the first use (zero-fill the whole buffer once); every call leaves them at
  * zero again, so later calls -- also for other shapes -- need no clearing.
  * The rest holds f32 partial sums.  Calls that share a workspace must not
- * overlap in time.
+ * overlap in time nor be made by two host threads at once.
  * Errors: as mxfp4_gemm, plus WORKSPACE (too small or null when needed). */
 MXFP4_API mxfp4_status_t mxfp4_gemm_ex(const void *A, const void *Bq_sh, const void *Bs_sh, void *C, int64_t M, int64_t N,
                              int64_t K, void *workspace, size_t workspace_bytes, mxfp4_stream_t stream);
@@ -321,9 +323,11 @@ MXFP4_API mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, cons
 /* Device memory of the routing and the grouped product.  Each of them takes */
 /* `workspace`, 256-byte aligned and of at least the stated bytes; its        */
 /* contents need no clearing and are lost, and calls that share it must not  */
-/* overlap in time.  NULL: the library's own workspace of (device, stream),  */
-/* as mxfp4_gemm has it: created or grown by the first call that needs more, */
-/* or ahead of time by mxfp4_reserve_bytes (before graph capture, say).      */
+/* overlap in time nor be made by two host threads at once.                  */
+/* NULL: the library's own workspace of (device, stream), as mxfp4_gemm has  */
+/* it: created or grown by the first call that needs more, or ahead of time  */
+/* by mxfp4_reserve_bytes (before graph capture, say), and kept by a call    */
+/* until its last launch is enqueued.                                        */
 MXFP4_API mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream);
 
 /* The router: which experts each token takes, with which weights, and the   */
