@@ -4,6 +4,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
 #include <cmath>
 #include <map>
 #include <mutex>
@@ -364,6 +365,15 @@ int alloc_workspace(int device, void *stream, size_t bytes, void **out) {
 
 Workspaces g_ws(alloc_workspace);
 
+// hipStreamPerThread is one handle for another stream in every thread, so a
+// workspace of it belongs to a thread: its number, which no later one takes.
+uint64_t thread_of(hipStream_t stream) {
+  if (stream != hipStreamPerThread) return 0;
+  static std::atomic<uint64_t> threads{0};
+  static thread_local const uint64_t mine = ++threads;
+  return mine;
+}
+
 }  // namespace
 
 namespace mxfp4 {
@@ -373,14 +383,14 @@ mxfp4_status_t ready_workspace(size_t need, hipStream_t stream) {
   int dev = 0;
   if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
   void *p = nullptr;
-  return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, &p);
+  return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, &p, thread_of(stream));
 }
 
 mxfp4_status_t hold_workspace(size_t need, hipStream_t stream, HeldWorkspace *out) {
   if (need == 0) return MXFP4_OK;
   int dev = 0;
   if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
-  return (mxfp4_status_t)g_ws.hold(dev, (void *)stream, need, &out->ptr, &out->lock);
+  return (mxfp4_status_t)g_ws.hold(dev, (void *)stream, need, &out->ptr, &out->lock, thread_of(stream));
 }
 
 }  // namespace mxfp4

@@ -1,4 +1,5 @@
-// Registry of library-owned workspaces, one per (device, stream).
+// Registry of library-owned workspaces, one per (device, stream); `thread`
+// tells streams apart that share one handle (0 otherwise).
 //
 // A buffer that has been handed out is never freed while the process runs:
 // a HIP graph captured earlier keeps its address, and replaying the graph
@@ -20,6 +21,7 @@
 #pragma once
 
 #include <stddef.h>
+#include <stdint.h>
 
 #include <memory>
 #include <mutex>
@@ -46,17 +48,17 @@ class WorkspacePool {
   // Buffer of at least `need` bytes (rounded up to 256) for (device,
   // stream); *out is null for need == 0.  Returns the allocator's status
   // (0 for success); on failure the registry is unchanged.
-  int get(int device, void *stream, size_t need, void **out) {
+  int get(int device, void *stream, size_t need, void **out, uint64_t thread = 0) {
     std::shared_ptr<std::mutex> unused;
-    return find(device, stream, need, out, &unused);
+    return find(device, stream, thread, need, out, &unused);
   }
 
   // As get, and returns once no other caller holds a buffer of (device,
   // stream); *lock then keeps it from others until it is released.  Locks
   // nothing for need == 0.
-  int hold(int device, void *stream, size_t need, void **out, Lock *lock) {
+  int hold(int device, void *stream, size_t need, void **out, Lock *lock, uint64_t thread = 0) {
     std::shared_ptr<std::mutex> busy;
-    if (int st = find(device, stream, need, out, &busy)) return st;
+    if (int st = find(device, stream, thread, need, out, &busy)) return st;
     // Growth by the holder waited for leaves *out retired, which serves as well.
     if (busy) *lock = Lock(std::move(busy));
     return 0;
@@ -84,18 +86,19 @@ class WorkspacePool {
   struct Entry {
     int device;
     void *stream;
+    uint64_t thread;
     void *ptr;
     size_t bytes;
     std::shared_ptr<std::mutex> busy;  // held by the call that uses the buffer
   };
 
-  int find(int device, void *stream, size_t need, void **out, std::shared_ptr<std::mutex> *busy) {
+  int find(int device, void *stream, uint64_t thread, size_t need, void **out, std::shared_ptr<std::mutex> *busy) {
     *out = nullptr;
     if (need == 0) return 0;
     need = (need + 255) & ~(size_t)255;
     std::lock_guard<std::mutex> lk(mu_);
     for (Entry &e : live_) {
-      if (e.device != device || e.stream != stream) continue;
+      if (e.device != device || e.stream != stream || e.thread != thread) continue;
       if (e.bytes < need) {
         size_t bytes = e.bytes * 2 > need ? e.bytes * 2 : need;
         void *p = nullptr;
@@ -110,7 +113,7 @@ class WorkspacePool {
     }
     void *p = nullptr;
     if (int st = alloc_(device, stream, need, &p)) return st;
-    live_.push_back(Entry{device, stream, p, need, std::make_shared<std::mutex>()});
+    live_.push_back(Entry{device, stream, thread, p, need, std::make_shared<std::mutex>()});
     *out = p;
     *busy = live_.back().busy;
     return 0;

@@ -177,6 +177,7 @@ MXFP4_API const char *mxfp4_gemm_q_schedule_name(int64_t M, int64_t N, int64_t K
 /* size, so what stays behind is at most about the live buffer's size).      */
 /* A call keeps the workspace to itself until its last launch is enqueued, so */
 /* host threads may call on one stream at once; a second one waits.          */
+/* hipStreamPerThread is a stream, and has a workspace, of each thread.      */
 /* The device is the calling thread's current device, which `stream` must    */
 /* belong to.  Results are deterministic: the split-K partial sums */
 /* are added in a fixed order (unless an "_at" schedule is forced by         */

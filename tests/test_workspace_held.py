@@ -1,7 +1,7 @@
 """A call that hands data from one launch to the next through the library's
 workspace keeps it until its last launch is enqueued: host threads that call
-on one stream cannot mix their launches, and threads on different streams do
-not wait for each other.  Host-only: the entry points are built here with
+on one stream cannot mix their launches, threads on different streams do not
+wait for each other, and the per-thread stream is a stream of each thread.  Host-only: the entry points are built here with
 g++ against stand-ins for HIP and the launchers, once plainly and once with
 ThreadSanitizer."""
 import os
@@ -36,7 +36,7 @@ def run(exe, what):
     return r.stderr
 
 
-@pytest.mark.parametrize("what", ["one_stream", "two_streams"])
+@pytest.mark.parametrize("what", ["one_stream", "two_streams", "stream_per_thread"])
 def test_launches_of_two_calls_do_not_mix(check, what):
     run(check, what)
 

@@ -135,8 +135,20 @@ int main(int argc, char **argv) {
     threads(2, 1, [](int t) -> void * { return (void *)(uintptr_t)(0x40 + 0x40 * t); });
     CHECK(g_errors.load() == 0 && g_met.load() == 2);
     CHECK(g_mixed.load() == 0);
+  } else if (!strcmp(what, "stream_per_thread")) {
+    // one handle for another stream in every thread: no buffer in common
+    threads(4, 40, [](int) -> void * { return hipStreamPerThread; });
+    CHECK(g_errors.load() == 0 && g_calls.load() == 160 && g_used.size() == 4);
+    std::set<void *> all;
+    size_t n = 0;
+    for (auto &u : g_used) {
+      n += u.second.size();
+      all.insert(u.second.begin(), u.second.end());
+    }
+    CHECK(n == all.size());
+    CHECK(mxfp4_reserve_bytes(1000, hipStreamPerThread) == MXFP4_OK);
   } else {
-    fprintf(stderr, "one_stream or two_streams\n");
+    fprintf(stderr, "one_stream, two_streams or stream_per_thread\n");
     return 2;
   }
   printf("%s ok\n", what);
