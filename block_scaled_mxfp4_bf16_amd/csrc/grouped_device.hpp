@@ -18,34 +18,29 @@
 // than E offsets to scan.
 #pragma once
 
+#include "experts_bounds.hpp"
 #include "experts_device.hpp"
 #include "experts_internal.hpp"
 
 namespace mxfp4 {
 
-// plan[0].x is the number of units, plan[1 + u] unit u.
-struct Unit {
-  int expert;
-  int row;   // first output row
-  int rows;  // output rows from `row` to the end of the group
-  int tile;  // its first 16-row tile in the workspace
-  int index; // its number among the expert's units
-};
-
-// An entry's first word holds the expert and, above it, the unit's number
-// among the expert's (at most 2^20 rows of 16 a unit: 17 bits).
-constexpr int kExpertBits = 12, kMaxExperts = 1 << kExpertBits;
-
-// Entries are read through the scalar cache: the index is the same in every
-// lane, and the reads do not queue behind the operand loads.
+// plan[0].x is the number of units, plan[1 + u] unit u.  Entries are read
+// through the scalar cache: the index is the same in every lane, and the reads
+// do not queue behind the operand loads.  Both are held to this call's sizes.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+template <int UNIT_ROWS>
 __device__ __forceinline__ Unit plan_entry(const GroupedArgs &a, int i) {
   const i32x4 v = ((const __attribute__((address_space(4))) i32x4 *)a.plan)[i];
-  return Unit{v.x < 0 ? -1 : v.x & (kMaxExperts - 1), v.y, v.z, v.w, v.x >> kExpertBits};
+  int w[4] = {v.x, v.y, v.z, v.w};
+  // what is checked is what is used: no second read in its place
+  asm("" : "+s"(w[0]), "+s"(w[1]), "+s"(w[2]), "+s"(w[3]));
+  return unit_of(w[0], w[1], w[2], w[3], a.R, a.E, 4 * a.quads, UNIT_ROWS);
 }
 
 __device__ __forceinline__ int unit_count(const GroupedArgs &a) {
-  return *(const __attribute__((address_space(4))) int *)a.plan;
+  int n = *(const __attribute__((address_space(4))) int *)a.plan;
+  asm("" : "+s"(n));
+  return within(n, 0, a.max_units);
 }
 
 // Rows of expert e, clamped to [0, R): whatever the offsets hold, no group

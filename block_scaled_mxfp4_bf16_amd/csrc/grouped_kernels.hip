@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
   for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
     const int index = (int)(item / n_tiles);
     const int n_tile = (int)(item - (int64_t)index * n_tiles);
-    const Unit u = plan_entry(a, 1 + index);
+    const Unit u = plan_entry<16>(a, 1 + index);
     if (u.expert < 0) continue;
 
     const int rows = u.rows < 16 ? u.rows : 16;

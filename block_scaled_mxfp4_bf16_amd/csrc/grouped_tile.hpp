@@ -110,19 +110,13 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
 
   auto enter = [&]() {
     none = next_item >= end;
-    int u = none ? 0 : next_item / n_tiles, n_tile = 0;
-    unit = plan_entry(a, 1 + u);
+    const int u = none ? 0 : next_item / n_tiles;
+    int n_tile = 0;
+    unit = plan_entry<16 * UT>(a, 1 + u);
     if (!none && unit.expert >= 0) {
-      const int first = u - unit.index;
-      const int all = unit.index + ((unit.rows + 16 * UT - 1) / (16 * UT));
-      const int in_expert = next_item - first * n_tiles;
-      const int block = in_expert / (kBlockUnits * n_tiles);
-      const int in_block = in_expert - block * kBlockUnits * n_tiles;
-      const int listed = all < units - first ? all : units - first;
-      const int width = listed - kBlockUnits * block < kBlockUnits ? listed - kBlockUnits * block : kBlockUnits;
-      n_tile = in_block / width;
-      u = first + kBlockUnits * block + in_block - n_tile * width;
-      unit = plan_entry(a, 1 + u);
+      const TilePlace at = tile_place(next_item, n_tiles, units, u, unit.index, unit.rows, 16 * UT, kBlockUnits);
+      n_tile = at.column;
+      unit = plan_entry<16 * UT>(a, 1 + at.unit);
     }
     next_item += stride;
     const int tiles = none || unit.expert < 0 ? 0 : (unit.rows < 16 * UT ? (unit.rows + 15) >> 4 : UT);

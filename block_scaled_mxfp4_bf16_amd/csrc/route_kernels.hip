@@ -22,14 +22,13 @@
 // logits) and 6.6 to place; one token of 64 experts 5.0 us, one launch.
 #include <type_traits>
 
+#include "experts_bounds.hpp"
 #include "experts_device.hpp"
 #include "experts_internal.hpp"
 
 namespace mxfp4 {
 
 namespace {
-
-constexpr int kMaxExperts = kRouteMaxExperts;
 
 // The value of lane (l + N) % 16 of the lane's row of 16.
 template <int N>
@@ -264,7 +263,8 @@ __device__ __forceinline__ int scan_experts(int *v, int E) {
 // bits of the id.  next[e] is the first free place of expert e.
 template <int THREADS>
 __device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int64_t p1, const int *next,
-                                            int (*wave_next)[kMaxExperts]) {
+                                            int (*wave_next)[kRouteMaxExperts]) {
+  const int pairs = a.T * a.k;
   constexpr int W = THREADS / 64;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -299,7 +299,8 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int6
     const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
     if (id >= 0) {
       const int at = wave_next[wave][id] + before;
-      a.rows[at] = (int32_t)mine;
+      // always, unless another call has written to the counts
+      if ((unsigned)at < (unsigned)pairs) a.rows[at] = (int32_t)mine;
       a.pos[mine] = at;
     } else if (mine < hi) {
       a.pos[mine] = -1;
@@ -319,7 +320,7 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int6
 // once, and a block has at most 4096 tokens).
 template <int L, int V, bool BIAS>
 __global__ __launch_bounds__(512) void route_choose_kernel(const RouteArgs a) {
-  __shared__ int hist[kMaxExperts];
+  __shared__ int hist[kRouteMaxExperts];
   for (int e = threadIdx.x; e < a.E; e += 512) hist[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * a.per_block;
@@ -333,9 +334,9 @@ __global__ __launch_bounds__(512) void route_choose_kernel(const RouteArgs a) {
 // expert) a load, 8 loads in flight: one a lane and dependent, as in a plain
 // loop, they took 30 us of the 35 of 256 blocks of 128 experts.
 __global__ __launch_bounds__(512) void route_place_kernel(const RouteArgs a) {
-  __shared__ int next[kMaxExperts];    // all counts, then first place, of each expert
-  __shared__ int before[kMaxExperts];  // pairs of the expert in earlier blocks
-  __shared__ int wave_next[8][kMaxExperts];
+  __shared__ int next[kRouteMaxExperts];    // all counts, then first place, of each expert
+  __shared__ int before[kRouteMaxExperts];  // pairs of the expert in earlier blocks
+  __shared__ int wave_next[8][kRouteMaxExperts];
   __shared__ int used;
   for (int e = threadIdx.x; e < a.E; e += 512) next[e] = before[e] = 0;
   __syncthreads();
@@ -375,7 +376,7 @@ __global__ __launch_bounds__(512) void route_place_kernel(const RouteArgs a) {
   __syncthreads();
   if (threadIdx.x < 64) {
     const int n = scan_experts(next, a.E);
-    if (threadIdx.x == 0) used = n;
+    if (threadIdx.x == 0) used = within(n, 0, a.T * a.k);
   }
   __syncthreads();
   if (blockIdx.x == 0) {
@@ -395,8 +396,8 @@ __global__ __launch_bounds__(512) void route_place_kernel(const RouteArgs a) {
 // Few tokens: all of it in one workgroup and one launch.
 template <int L, int V, bool BIAS>
 __global__ __launch_bounds__(512) void route_small_kernel(const RouteArgs a) {
-  __shared__ int next[kMaxExperts];
-  __shared__ int wave_next[8][kMaxExperts];
+  __shared__ int next[kRouteMaxExperts];
+  __shared__ int wave_next[8][kRouteMaxExperts];
   __shared__ int used;
   for (int e = threadIdx.x; e < a.E; e += 512) next[e] = 0;
   __syncthreads();
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(512) void route_small_kernel(const RouteArgs a) {
   __syncthreads();  // the ids this block wrote are read back below
   if (threadIdx.x < 64) {
     const int n = scan_experts(next, a.E);
-    if (threadIdx.x == 0) used = n;
+    if (threadIdx.x == 0) used = within(n, 0, a.T * a.k);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += 512) a.offsets[e] = next[e];
