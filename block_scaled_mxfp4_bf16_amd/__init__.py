@@ -415,6 +415,13 @@ def _on_gpu(dev):
         raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (dev, _current_device()))
 
 
+def _workspace(ws, dev):
+    """Address and bytes of a caller's workspace."""
+    if ws.get_device() != dev or not ws.is_contiguous() or ws.is_meta:
+        raise ValueError("workspace must be a contiguous tensor on %s" % _device(dev))
+    return ws.data_ptr(), ws.nbytes
+
+
 def prepare_experts(B, stream=None):
     """bf16 [E, N, K] cuda tensor -> (Bw [E, N/16, (K/2)*16], Bs [E, ...]): each matrix prepared as by prepare_b."""
     import torch
@@ -463,14 +470,21 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
     return out
 
 
-def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: bool = False, out=None, stream=None):
+def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: bool = False, out=None, stream=None,
+                 workspace=None):
     """C[p] = Q(A[row(p)]) * B_e^T for offsets[e] <= p < offsets[e + 1], bf16.
 
     A [a_rows, K] bf16 with contiguous rows; Bw, Bs E matrices from
     prepare_experts; offsets int32 [E + 1].  row(p) is rows[p] // repeat (int32
     [R], from moe_route with repeat = k), or p without rows.  gated: N/2
-    columns, silu(first half) * second.  Rows of no group are zero."""
+    columns, silu(first half) * second.  Rows of no group are zero.
+
+    workspace: a cuda tensor of mxfp4_gemm_grouped_workspace_bytes(R, K, E)
+    bytes that no other work uses meanwhile; without one the library's of the
+    stream serves.  A graph keeps the one it was captured with, so graphs that
+    are replayed at the same time need one each."""
     L = _lib if _torch else _start()
+    ws, ws_bytes = None, 0
     torch = _torch
     T, K, lda, dev = _matrix(A, "A", "rows, K")
     if A.dtype != torch.bfloat16:
@@ -491,9 +505,11 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
         ldc = _rows_of(out, "out", R, cols, dev)
         if out.dtype != torch.bfloat16:
             raise TypeError("out must be bf16, not %s" % out.dtype)
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace, dev)
     _on_gpu(dev)
     rc = L.mxfp4_gemm_grouped(A.data_ptr(), lda, T, Bw.data_ptr(), Bs.data_ptr(), E, offsets.data_ptr(), rows, repeat,
-                                    out.data_ptr(), ldc, R, N, K, 1 if gated else 0, None, 0,
+                                    out.data_ptr(), ldc, R, N, K, 1 if gated else 0, ws, ws_bytes,
                                     _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_gemm_grouped")
@@ -503,7 +519,8 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
 _scores = {"softmax": 0, "sigmoid": 1}
 
 
-def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bool = True, out=None, stream=None):
+def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bool = True, out=None, stream=None,
+              workspace=None):
     """The k experts of each token and the (token, choice) pairs sorted by expert.
 
     logits [T, E], bf16, f16 or f32, with contiguous rows; score "softmax" or
@@ -514,8 +531,10 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
       weights f32 [T, k], g of the chosen, renormalized to sum 1 if asked
       offsets int32 [E + 1], where each expert's pairs lie in rows
       rows    int32 [T * k], the pair t * k + j at each sorted place, or -1
-      pos     int32 [T, k], the sorted place of each pair, or -1"""
+      pos     int32 [T, k], the sorted place of each pair, or -1
+    workspace: as for gemm_grouped, of mxfp4_moe_route_workspace_bytes(T, E) bytes."""
     L = _lib if _torch else _start()
+    ws, ws_bytes = None, 0
     torch = _torch
     T, E, ld, dev = _matrix(logits, "logits", "T, E")
     lt = _type(logits)
@@ -538,9 +557,11 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
         _array(offsets, torch.int32, "offsets", E + 1, dev)
         _array(rows, torch.int32, "rows", n, dev)
         _array(pos, torch.int32, "pos", n, dev)
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace, dev)
     _on_gpu(dev)
     rc = L.mxfp4_moe_route(logits.data_ptr(), lt, ld, bias, T, E, k, kind, 1 if renormalize else 0, ids.data_ptr(),
-                                 weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), None, 0,
+                                 weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), ws, ws_bytes,
                                  _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_moe_route")

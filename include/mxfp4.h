@@ -175,6 +175,9 @@ MXFP4_API const char *mxfp4_gemm_q_schedule_name(int64_t M, int64_t N, int64_t K
 /* stays allocated until the process ends, so a HIP graph captured before    */
 /* the growth still replays into valid memory (growth at least doubles the   */
 /* size, so what stays behind is at most about the live buffer's size).      */
+/* A graph keeps the workspace of the stream it was captured on wherever it  */
+/* is replayed: two graphs captured on one stream must not run at the same   */
+/* time (mxfp4_gemm_ex takes a workspace for each).                          */
 /* A call keeps the workspace to itself until its last launch is enqueued, so */
 /* host threads may call on one stream at once; a second one waits.          */
 /* hipStreamPerThread is a stream, and has a workspace, of each thread.      */
@@ -329,6 +332,10 @@ MXFP4_API mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, cons
 /* it: created or grown by the first call that needs more, or ahead of time  */
 /* by mxfp4_reserve_bytes (before graph capture, say), and kept by a call    */
 /* until its last launch is enqueued.                                        */
+/* A graph keeps the workspace of the stream that it was captured on, on     */
+/* whatever stream it is replayed.  Two graphs captured on one stream, or one */
+/* and calls on that stream, must not run at the same time unless each was   */
+/* given a workspace of its own: their results would have no meaning.        */
 MXFP4_API mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream);
 
 /* The router: which experts each token takes, with which weights, and the   */
