@@ -265,17 +265,46 @@ def mxfp4_moe_combine(y, y_type: int, ld_y: int, rows: int, weights, pos, residu
 
 # ---- tensor conveniences (allocate outputs with torch, then call the above) --
 
+def _allocator(stream):
+    """torch.empty for outputs that a kernel on `stream` writes.
+
+    They lie in that stream's memory: memory of the current stream may still
+    be in use by work there that `stream` does not wait for, and would be
+    handed out again when the tensor is dropped, though the kernel may not
+    have run yet.  They are recorded as used on the current stream, which is
+    where the caller goes on with them."""
+    import torch
+    if stream is None:
+        return torch.empty
+    handle = _stream(stream)
+    if handle == _current_stream():
+        return torch.empty
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    current = torch.cuda.current_stream()
+
+    def empty(*args, **kwargs):
+        with torch.cuda.stream(stream):
+            t = torch.empty(*args, **kwargs)
+        if t.is_cuda:
+            t.record_stream(current)
+        return t
+
+    return empty
+
+
 def quantize(x, shuffled_scales: bool = False, stream=None):
     """bf16 [rows, K] cuda tensor -> (q uint8 [rows, K/2], scales uint8)."""
     import torch
+    empty = _allocator(stream)
     rows, K = x.shape
     assert x.dtype == torch.bfloat16 and x.is_contiguous()
-    q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+    q = empty((rows, K // 2), dtype=torch.uint8, device=x.device)
     if shuffled_scales:
-        s = torch.empty(mxfp4_shuffled_scale_bytes(rows, K), dtype=torch.uint8, device=x.device)
+        s = empty(mxfp4_shuffled_scale_bytes(rows, K), dtype=torch.uint8, device=x.device)
         s = s.view(-1, ((K // 32 + 7) // 8) * 32)
     else:
-        s = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        s = empty((rows, K // 32), dtype=torch.uint8, device=x.device)
     mxfp4_quantize(x, rows, K, q, s, shuffled_scales, stream)
     return q, s
 
@@ -283,10 +312,11 @@ def quantize(x, shuffled_scales: bool = False, stream=None):
 def preshuffle_b(bq, bs_raw, stream=None):
     """Quantized B (natural layouts) -> (Bw [N/16, (K/2)*16], Bs shuffled)."""
     import torch
+    empty = _allocator(stream)
     N, KB = bq.shape
     K = KB * 2
-    bw = torch.empty((N // 16, KB * 16), dtype=torch.uint8, device=bq.device)
-    bs = torch.empty(mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=bq.device)
+    bw = empty((N // 16, KB * 16), dtype=torch.uint8, device=bq.device)
+    bs = empty(mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=bq.device)
     bs = bs.view(-1, ((K // 32 + 7) // 8) * 32)
     mxfp4_preshuffle_b(bq, bs_raw, N, K, bw, bs, stream)
     return bw, bs
@@ -295,10 +325,11 @@ def preshuffle_b(bq, bs_raw, stream=None):
 def prepare_b(b, stream=None):
     """bf16 [N, K] cuda tensor -> (Bw [N/16, (K/2)*16], Bs shuffled), in one launch."""
     import torch
+    empty = _allocator(stream)
     N, K = b.shape
     assert b.dtype == torch.bfloat16 and b.is_contiguous()
-    bw = torch.empty((N // 16, (K // 2) * 16), dtype=torch.uint8, device=b.device)
-    bs = torch.empty(mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=b.device)
+    bw = empty((N // 16, (K // 2) * 16), dtype=torch.uint8, device=b.device)
+    bs = empty(mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=b.device)
     bs = bs.view(-1, ((K // 32 + 7) // 8) * 32)
     mxfp4_prepare_b(b, N, K, bw, bs, stream)
     return bw, bs
@@ -309,7 +340,7 @@ def gemm_q(Aq, As, Bw, Bs, N: int, out=None, stream=None):
     import torch
     M, KB = Aq.shape
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=Aq.device)
+        out = _allocator(stream)((M, N), dtype=torch.bfloat16, device=Aq.device)
     mxfp4_gemm_q(Aq, As, Bw, Bs, out, M, N, 2 * KB, stream)
     return out
 
@@ -320,7 +351,7 @@ def gemm(A, Bw, Bs, N: int, out=None, stream=None):
     M, K = A.shape
     assert A.dtype == torch.bfloat16 and A.is_contiguous()
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _allocator(stream)((M, N), dtype=torch.bfloat16, device=A.device)
     mxfp4_gemm(A, Bw, Bs, out, M, N, K, stream)
     return out
 
@@ -427,8 +458,9 @@ def prepare_experts(B, stream=None):
     import torch
     E, N, K = B.shape
     assert B.dtype == torch.bfloat16 and B.is_contiguous()
-    bw = torch.empty((E, N // 16, (K // 2) * 16), dtype=torch.uint8, device=B.device)
-    bs = torch.empty(E * mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=B.device)
+    empty = _allocator(stream)
+    bw = empty((E, N // 16, (K // 2) * 16), dtype=torch.uint8, device=B.device)
+    bs = empty(E * mxfp4_shuffled_scale_bytes(N, K), dtype=torch.uint8, device=B.device)
     bs = bs.view(E, -1, ((K // 32 + 7) // 8) * 32)
     for e in range(E):
         mxfp4_prepare_b(B[e], N, K, bw[e], bs[e], stream)
@@ -456,7 +488,7 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
         raise ValueError("%d matrices need ids" % E)
     cols = N // 2 if gated else N
     if out is None:
-        out = torch.empty((M, cols), dtype=out_dtype or x.dtype, device=x.device)
+        out = (torch.empty if stream is None else _allocator(stream))((M, cols), dtype=out_dtype or x.dtype, device=x.device)
         ldy = cols
     else:
         ldy = _rows_of(out, "out", M, cols, dev)
@@ -499,7 +531,7 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
         R = T
     cols = N // 2 if gated else N
     if out is None:
-        out = torch.empty((R, cols), dtype=torch.bfloat16, device=A.device)
+        out = (torch.empty if stream is None else _allocator(stream))((R, cols), dtype=torch.bfloat16, device=A.device)
         ldc = cols
     else:
         ldc = _rows_of(out, "out", R, cols, dev)
@@ -547,8 +579,9 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
     n = T * k
     if out is None:
         i32 = dict(dtype=torch.int32, device=logits.device)
-        out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=logits.device),
-               torch.empty(E + 1, **i32), torch.empty(n, **i32), torch.empty((T, k), **i32))
+        empty = torch.empty if stream is None else _allocator(stream)
+        out = (empty((T, k), **i32), empty((T, k), dtype=torch.float32, device=logits.device),
+               empty(E + 1, **i32), empty(n, **i32), empty((T, k), **i32))
         ids, weights, offsets, rows, pos = out
     else:
         ids, weights, offsets, rows, pos = out
@@ -590,7 +623,7 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
         raise ValueError("y has %d rows, %d tokens of %d choices need %d" % (R, T, k, T * k))
     if out is None:
         dtype = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
-        out = torch.empty((T, N), dtype=dtype, device=y.device)
+        out = (torch.empty if stream is None else _allocator(stream))((T, N), dtype=dtype, device=y.device)
         ld_out = N
     else:
         ld_out = _rows_of(out, "out", T, N, dev)
