@@ -417,6 +417,13 @@ def _rows_of(t, what, rows, cols, dev):
                      (what, rows, cols, _device(dev)))
 
 
+def _no_gradients(what):
+    """For an input that requires gradients: refuses a call that autograd would follow."""
+    if _torch.is_grad_enabled():
+        raise RuntimeError("%s requires gradients, and the expert operators have none: detach it, or call under "
+                           "torch.no_grad()" % what)
+
+
 @functools.lru_cache(maxsize=1024)
 def _prepared_bytes(N, K):
     return mxfp4_packed_bytes(N, K), mxfp4_shuffled_scale_bytes(N, K)
@@ -479,6 +486,8 @@ def gemv(x, Bw, Bs, N: int, ids=None, repeat: int = 1, gated: bool = False, out=
     torch = _torch
     tokens, K, ldx, dev = _matrix(x, "x", "M, K")
     xt = _type(x)
+    if x.requires_grad:
+        _no_gradients("x")
     E = _prepared(Bw, Bs, N, K, dev)
     M = tokens * repeat
     if ids is not None:
@@ -521,6 +530,8 @@ def gemm_grouped(A, Bw, Bs, offsets, N: int, rows=None, repeat: int = 1, gated: 
     T, K, lda, dev = _matrix(A, "A", "rows, K")
     if A.dtype != torch.bfloat16:
         raise TypeError("A must be bf16, not %s" % A.dtype)
+    if A.requires_grad:
+        _no_gradients("A")
     E = _prepared(Bw, Bs, N, K, dev)
     _array(offsets, torch.int32, "offsets", E + 1, dev)
     if rows is not None:
@@ -570,11 +581,15 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, renormalize: bo
     torch = _torch
     T, E, ld, dev = _matrix(logits, "logits", "T, E")
     lt = _type(logits)
+    if logits.requires_grad:
+        _no_gradients("logits")
     kind = _scores.get(score)
     if kind is None:
         raise ValueError("score must be 'softmax' or 'sigmoid', not %r" % (score,))
     if bias is not None:
         _array(bias, torch.float32, "bias", E, dev)
+        if bias.requires_grad:
+            _no_gradients("bias")
         bias = bias.data_ptr()
     n = T * k
     if out is None:
@@ -616,6 +631,8 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
     T, k = weights.shape
     yt = _type(y)
     _array(weights, torch.float32, "weights", T * k, dev)
+    if y.requires_grad or weights.requires_grad:
+        _no_gradients("y" if y.requires_grad else "weights")
     if pos is not None:
         _array(pos, torch.int32, "pos", T * k, dev)
         pos = pos.data_ptr()
@@ -632,6 +649,8 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
         ld_res = _rows_of(residual, "residual", T, N, dev)
         if residual.dtype != out.dtype:
             raise TypeError("residual is %s, out %s" % (residual.dtype, out.dtype))
+        if residual.requires_grad:
+            _no_gradients("residual")
         residual = residual.data_ptr()
     ot = _type(out)
     _on_gpu(dev)
