@@ -26,6 +26,14 @@ __device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
   b = r.y;
 }
 
+// Between LDS accesses of different lanes of one wave to the same place: the
+// hardware does a wave's accesses in order, so this only keeps the compiler
+// from moving one past the other, which a lane's own addresses would allow.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // silu(g) * u.  exp(-g) overflows to infinity for g below -88, where the
 // quotient is the right -0.  The reciprocal is the hardware's, within 1 ulp:
 // next to the exponential's own error it costs nothing, and a divide takes ten

@@ -244,6 +244,7 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
         *place(me & 31, 2 * part + (me >> 5)) = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
         __builtin_amdgcn_sched_barrier(0);  // few values at a time: the registers are full
       }
+      wave_lds_fence();
 #pragma unroll
       for (int s = 0; s < CHUNKS / 2; ++s) {
         const int row = s * (64 / CHUNKS) + first_row;
@@ -259,6 +260,7 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
           }
         }
       }
+      wave_lds_fence();  // before the next rows
       __builtin_amdgcn_sched_barrier(0);
     }
   };

@@ -305,11 +305,9 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int6
     } else if (mine < hi) {
       a.pos[mine] = -1;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
     if (id >= 0 && before == 0) wave_next[wave][id] += __builtin_popcountll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
   }
 }
 
