@@ -14,11 +14,12 @@
 //
 // Lane l of the load holds column l % 16 and group 4 * step + l / 16: all 32
 // elements of one group, so one scale per lane.
-//   bf16 rows  the convert applies the scale: e2m1 * 2^e is exact in bf16.
-//              Product i takes elements 8i..8i+7 of the lane's group.
+//   bf16 rows  the convert applies the scale: e2m1 * 2^e is exact in bf16 (down
+//              to 2^-128: subnormals count; beyond 2^128 see `compute`).  Product i takes elements 8i..8i+7 of the lane's group.
 //   f32 rows   as bf16, with x cut into three bf16 parts of 8 significand
-//              bits each: hi + mid + lo = x exactly, so the only rounding is
-//              that of the f32 sums, as in a product of f32 by f32.
+//              bits each: hi + mid + lo = x exactly down to the last bit of
+//              bf16's subnormals, 2^-133, so that the only rounding is that of
+//              the f32 sums, as in a product of f32 by f32.
 //   f16 rows   a scaled weight may leave f16's range, so the codes are
 //              converted unscaled and the f32 sum of each group is scaled
 //              instead.  That needs products that stay within one group: the
@@ -31,6 +32,8 @@
 // Measured: 32 expert rows of 4096 x 2048, gated, 22.8 us, 5.2 TB/s of weights;
 // one row of 7168 x 7168 6.3 us, 4.4 TB/s with the launch; one row of 4096 x 512
 // 3.0 us, a launch and one round of loads.
+#include <type_traits>
+
 #include "experts_device.hpp"
 #include "experts_internal.hpp"
 
@@ -39,6 +42,10 @@ namespace mxfp4 {
 namespace {
 
 enum { kBf16 = 0, kF16 = 1, kF32 = 2 };
+
+// Bits of the largest scale, as f32, with which bf16 holds every weight (6 *
+// 2^125), and of the scale that stands for NaN.
+constexpr uint32_t kLargestScale = 252u << 23, kNanScale = 255u << 23;
 
 // Eight weights of one dword of codes as bf16, scaled by a power of two.
 __device__ __forceinline__ bf16x8 weights_bf16(uint32_t w, float scale) {
@@ -65,8 +72,8 @@ __device__ __forceinline__ f16x8 weights_f16(uint32_t w) {
   return u.v;
 }
 
-// Eight f32 values as three bf16 vectors whose sum is exact: each part is
-// the top 16 bits of what the parts before it left.  Infinities and NaN stay
+// Eight f32 values as three bf16 vectors whose sum is exact (bits below 2^-133
+// aside): each part is the top 16 bits of what the parts before it left.  Infinities and NaN stay
 // in the first part (inf - inf would make them NaN).
 __device__ __forceinline__ void split_f32(const u32x4 &p, const u32x4 &q, bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
   const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
@@ -192,7 +199,13 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a, int fir
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) acc[nt] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int ks, const Stage &st) {
+  // bf16 and f32 rows: bf16 does not hold every weight of a scale beyond
+  // kLargestScale.  The steps note the largest scale; where it is beyond, which
+  // no model's weights are, the sums start again with kLargestScale in its
+  // place: all groups (pass 0), and such a one again (pass 1, and 2 and 3) until
+  // its 2 or 4 times are together.
+  uint32_t largest = 0;
+  auto compute = [&](int ks, const Stage &st, auto again, int pass) {
     bf16x8 part[XT == kF32 ? 3 : 1][4];
     if constexpr (XT == kF32) {
 #pragma unroll
@@ -227,8 +240,21 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a, int fir
           for (int r = 0; r < 4; ++r) acc[nt][r] += p[r] * sc;
         }
       } else {
-        const float sc = __uint_as_float(sbits);
-        const uint32_t d[4] = {st.b[nt].x, st.b[nt].y, st.b[nt].z, st.b[nt].w};
+        uint32_t d[4] = {st.b[nt].x, st.b[nt].y, st.b[nt].z, st.b[nt].w};
+        uint32_t scale = sbits;
+        if constexpr (decltype(again)::value) {
+          const int times = sbits > kLargestScale ? 1 << ((sbits - kLargestScale) >> 23) : 1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = times > pass ? d[i] : 0;
+          scale = sbits < kLargestScale ? sbits : kLargestScale;
+          // the four lanes of a column hold four of its groups, and of its sums
+          if ((__ballot(sbits == kNanScale) >> n16) & 0x0001000100010001ull)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[nt][r] = __builtin_nanf("");
+        } else {
+          largest = sbits > largest ? sbits : largest;
+        }
+        const float sc = __uint_as_float(scale);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bf16x8 w = weights_bf16(d[i], sc);
@@ -255,12 +281,26 @@ __global__ __launch_bounds__(64 * WK) void gemv_kernel(const GemvArgs a, int fir
   for (int it = 0; it + 1 < rounds; ++it) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      compute(wave + WK * (it * D + d), st[d]);
+      compute(wave + WK * (it * D + d), st[d], std::false_type{}, 0);
       load(wave + WK * ((it + 1) * D + d), st[d]);
     }
   }
 #pragma unroll
-  for (int d = 0; d < D; ++d) compute(wave + WK * ((rounds - 1) * D + d), st[d]);
+  for (int d = 0; d < D; ++d) compute(wave + WK * ((rounds - 1) * D + d), st[d], std::false_type{}, 0);
+  if constexpr (XT != kF16) {
+    if (__builtin_expect(__ballot(largest > kLargestScale) != 0, 0)) {
+      const int passes = __ballot(largest >= 254u << 23) ? 4 : 2;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int pass = 0; pass < passes; ++pass)
+#pragma unroll 1
+        for (int ks = wave; ks < steps; ks += WK) {
+          load(ks, st[0]);
+          compute(ks, st[0], std::true_type{}, pass);
+        }
+    }
+  }
 
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
