@@ -459,7 +459,7 @@ const char *mxfp4_status_string(mxfp4_status_t st) {
   switch (st) {
     case MXFP4_OK: return "MXFP4_OK";
     case MXFP4_ERR_INVALID_ARG: return "MXFP4_ERR_INVALID_ARG: null pointer, non-positive size or misaligned pointer";
-    case MXFP4_ERR_UNSUPPORTED: return "MXFP4_ERR_UNSUPPORTED: shape not handled (needs K % 64 == 0, N % 32 == 0)";
+    case MXFP4_ERR_UNSUPPORTED: return "MXFP4_ERR_UNSUPPORTED: a size outside what this entry point handles (mxfp4.h lists its limits)";
     case MXFP4_ERR_WORKSPACE: return "MXFP4_ERR_WORKSPACE: workspace missing or too small";
     case MXFP4_ERR_HIP: return "MXFP4_ERR_HIP: a HIP call or kernel launch failed";
   }

@@ -321,7 +321,8 @@ typedef enum { MXFP4_TYPE_BF16 = 0, MXFP4_TYPE_F16 = 1, MXFP4_TYPE_F32 = 2 } mxf
 /*         row stride not 16-byte aligned, B not 16-byte aligned, y not       */
 /*         aligned to its type);                                             */
 /*         UNSUPPORTED (K % 32 != 0, N % 16 != 0, gated with N % 32 != 0,    */
-/*         a matrix or 64 rows of x beyond 2^31 bytes, M beyond 2^20 rows).  */
+/*         a matrix or 64 rows of x beyond 2^31 bytes, M beyond 2^20 rows,   */
+/*         experts or repeat >= 2^31).                                        */
 MXFP4_API mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, const void *Bq_sh, const void *Bs_sh,
                                     const int32_t *ids, int64_t experts, void *y, int y_type, int64_t ldy, int64_t M,
                                     int64_t N, int64_t K, int64_t repeat, int gated, mxfp4_stream_t stream);
@@ -338,6 +339,7 @@ MXFP4_API mxfp4_status_t mxfp4_gemv(const void *x, int x_type, int64_t ldx, cons
 /* whatever stream it is replayed.  Two graphs captured on one stream, or one */
 /* and calls on that stream, must not run at the same time unless each was   */
 /* given a workspace of its own: their results would have no meaning.        */
+/* Errors of mxfp4_reserve_bytes: UNSUPPORTED (beyond 2^46 bytes); HIP.       */
 MXFP4_API mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream);
 
 /* The router: which experts each token takes, with which weights, and the   */
@@ -363,7 +365,8 @@ MXFP4_API mxfp4_status_t mxfp4_reserve_bytes(size_t bytes, mxfp4_stream_t stream
 /* T may be 0.  The result is the same every time.                            */
 /* Errors: INVALID_ARG (null, T < 0, E < 1, k < 1, k > E, ld < E, unknown     */
 /*         type or score, a pointer not aligned to its type);                */
-/*         UNSUPPORTED (E > 1024, k > 32, T > 2^20); WORKSPACE; HIP.          */
+/*         UNSUPPORTED (E > 1024, k > 32, T > 2^20, ld > 2^40); WORKSPACE;    */
+/*         HIP.                                                               */
 typedef enum { MXFP4_SCORE_SOFTMAX = 0, MXFP4_SCORE_SIGMOID = 1 } mxfp4_score_t;
 MXFP4_API size_t mxfp4_moe_route_workspace_bytes(int64_t T, int64_t E);
 MXFP4_API mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t ld, const float *bias, int64_t T,
@@ -393,7 +396,7 @@ MXFP4_API mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t
 /*         aligned, B not 16-byte aligned, C not 2-byte aligned);             */
 /*         UNSUPPORTED (K % 32 != 0, N % 16 != 0, gated with N % 32 != 0, a  */
 /*         matrix beyond 2^31 bytes, N, R or a_rows > 2^20, experts > 4096,    */
-/*         K > 2^17, ldc > 2^22, lda > 2^30);                                 */
+/*         K > 2^17, ldc > 2^22, lda > 2^30, repeat >= 2^31);                 */
 /*         WORKSPACE; HIP.                                                    */
 MXFP4_API size_t mxfp4_gemm_grouped_workspace_bytes(int64_t R, int64_t K, int64_t experts);
 MXFP4_API mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t a_rows, const void *Bq_sh,
@@ -415,7 +418,8 @@ MXFP4_API mxfp4_status_t mxfp4_gemm_grouped(const void *A, int64_t lda, int64_t 
 /* T may be 0 (and rows, which then, or with rows 0, may have a null y).     */
 /* Errors: INVALID_ARG (null, T or rows < 0, N < 1, k < 1, a row stride < N,  */
 /*         unknown type, a pointer not aligned to its type);                 */
-/*         UNSUPPORTED (N >= 2^31 - 4096, k > 2^20).                          */
+/*         UNSUPPORTED (N >= 2^31 - 4097, k > 2^20, T > 2^26, rows > 2^30,    */
+/*         a row stride > 2^30).                                              */
 MXFP4_API mxfp4_status_t mxfp4_moe_combine(const void *y, int y_type, int64_t ld_y, int64_t rows,
                                            const float *weights, const int32_t *pos, const void *residual,
                                            int64_t ld_res, void *out, int out_type, int64_t ld_out, int64_t T,
