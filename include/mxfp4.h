@@ -304,8 +304,8 @@ typedef enum { MXFP4_TYPE_BF16 = 0, MXFP4_TYPE_F16 = 1, MXFP4_TYPE_F32 = 2 } mxf
 /* Products of a few rows with MXFP4 weights, the activations unquantized:   */
 /*   y[r, n] = sum_k x[r, k] * B[n, k]                 (ids == NULL)          */
 /*   y[r, n] = sum_k x[r / repeat, k] * B_ids[r][n, k]  (ids != NULL)         */
-/* The weights are exact, the sums f32 in a fixed order, rounded once to y's */
-/* type.  Scale bytes 0 to 254 all count (weights up to 6 * 2^127); 255, which */
+/* The weights are exact, the sums f32 in an order that M, N, K and gated     */
+/* fix, rounded once to y's type.  Scale bytes 0 to 254 all count (weights up to 6 * 2^127); 255, which */
 /* stands for NaN, makes its columns of y NaN or infinite.  f32 rows count    */
 /* down to 2^-133.  Made for single tokens and small batches, whose time is that of    */
 /* reading B; any M is right.                                                */
@@ -380,7 +380,9 @@ MXFP4_API mxfp4_status_t mxfp4_moe_route(const void *logits, int x_type, int64_t
 /* with row(p) = rows[p] / repeat, or p where rows is NULL, and Q the         */
 /* quantization of mxfp4_quantize; and its gated form.  With the offsets and  */
 /* rows of mxfp4_moe_route and repeat = k it takes each token's row to the   */
-/* experts it chose.  f32 sums in a fixed order, rounded once.  The group    */
+/* experts it chose.  f32 sums in an order that R, N, K and experts fix,     */
+/* rounded once: calls of one size give a row the same bits whatever the     */
+/* other groups hold, calls of other sizes may differ in the last.  The group */
 /* sizes stay on the device; the host waits for nothing.                     */
 /*   A        [a_rows, K] bf16, rows lda elements apart             (input)  */
 /*   Bq_sh, Bs_sh  `experts` prepared matrices                       (input)  */
