@@ -626,9 +626,10 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
     L = _lib if _torch else _start()
     torch = _torch
     R, N, ld_y, dev = _matrix(y, "y", "rows, N")
-    if weights.dim() != 2:
+    shape = weights.shape
+    if len(shape) != 2:
         raise ValueError("weights must be [T, k]")
-    T, k = weights.shape
+    T, k = shape
     yt = _type(y)
     _array(weights, torch.float32, "weights", T * k, dev)
     if y.requires_grad or weights.requires_grad:
@@ -645,14 +646,17 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
     else:
         ld_out = _rows_of(out, "out", T, N, dev)
     ld_res = N
+    dtype = out.dtype
     if residual is not None:
         ld_res = _rows_of(residual, "residual", T, N, dev)
-        if residual.dtype != out.dtype:
-            raise TypeError("residual is %s, out %s" % (residual.dtype, out.dtype))
+        if residual.dtype != dtype:
+            raise TypeError("residual is %s, out %s" % (residual.dtype, dtype))
         if residual.requires_grad:
             _no_gradients("residual")
         residual = residual.data_ptr()
-    ot = _type(out)
+    ot = _types.get(dtype)
+    if ot is None:
+        raise TypeError("expected a bf16, f16 or f32 out, got %s" % dtype)
     _on_gpu(dev)
     rc = L.mxfp4_moe_combine(y.data_ptr(), yt, ld_y, R, weights.data_ptr(), pos, residual, ld_res, out.data_ptr(), ot,
                                    ld_out, T, k, N, _current_stream() if stream is None else _stream(stream))
