@@ -5,7 +5,7 @@
 // Reading y bounds it.  A thread takes 16 bytes (8 columns) of a token; the
 // loads of all choices (in runs of kAhead) go out before the first is used,
 // so a token pays the memory latency once, not once per choice.  Measured: 8
-// rows of 2048 for 4096 tokens 28.5 us, 5.9 TB/s; 8 rows of 7168 for 4 tokens 4.6
+// rows of 2048 for 4096 tokens 28.6 us, 5.9 TB/s; 8 rows of 7168 for 4 tokens 4.4
 // us, two dependent loads behind a launch.
 #include "experts_device.hpp"
 #include "experts_internal.hpp"

@@ -29,9 +29,12 @@
 // The waves of a workgroup split K and add their tiles through LDS in wave
 // order; sums are f32, rounded once to y's type.
 //
-// Measured: 32 expert rows of 4096 x 2048, gated, 22.8 us, 5.2 TB/s of weights;
-// one row of 7168 x 7168 6.3 us, 4.4 TB/s with the launch; one row of 4096 x 512
-// 3.0 us, a launch and one round of loads.
+// Measured, a call among others, weights partly in the caches: 32 expert rows of
+// 4096 x 2048, gated, 22.5 us, 5.2 TB/s of weights; one row of 7168 x 7168 6.3 us,
+// 4.4 TB/s with the launch; the kernel of one row of 4096 x 512 2.9 us, a launch and
+// one round of loads.  f32 rows, three products a step, in a graph over fresh
+// weights: one row of 7168 x 7168 17.3 us, 32 expert rows 40.8; f16 rows 8.8 and 25.9,
+// bf16 rows there 6.8 and 23.7.
 #include <type_traits>
 
 #include "experts_device.hpp"
@@ -340,6 +343,7 @@ static hipError_t run_gemv(const GemvArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The times below are those of calls in a graph over weights not read before.
 // 16 rows a workgroup whatever M is: reading B again for the next 16, from L2,
 // cost no more than tiles of 32 or 64 rows with their fewer workgroups (256
 // rows of 4096 x 4096, bf16: 23.5 us, 22.5 and 23.7), and less for few rows.

@@ -132,10 +132,10 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const GroupedArgs a, int
 // columns.  Units of 16 rows also where groups hold more: 64-row units read
 // the weights once instead of up to four times, but from L2 those repeats cost
 // less than the workgroups they spare (771 rows of 16 experts, 2112 x 704: 10.0
-// us with 64 rows, 8.4 with 16).  256 rows of 64 experts, 4096 x 2048: 45.0 us, 6.2
-// TB/s of weights; 32 columns or 8 waves instead (weights through the caches, then
-// 46.8): 48.9 and 46.4, but 17.2 and 17.5 for 15.2 of 700 rows of 32 experts, 4096 x
-// 1024.
+// us with 64 rows, 8.4 with 16).  256 rows of 64 experts, 4096 x 2048: 42 to 45 us
+// by the run, 6.2 TB/s of weights and more.  With the weights through the caches,
+// then 46.8 us: 32 columns or 8 waves instead 48.9 and 46.4, but 17.2 and 17.5 for
+// 15.2 of 700 rows of 32 experts, 4096 x 1024.
 // ONCE: weights that no cache will hold until they are read again go past them.
 template <int NT, int WK, bool ONCE>
 __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedArgs a, int n_tiles) {
@@ -252,12 +252,17 @@ __global__ __launch_bounds__(64 * WK) void grouped_stream_kernel(const GroupedAr
 // Workgroups of a launch (threads of a grid dimension are limited to 2^32).
 constexpr int64_t kMaxGrid = 1 << 22;
 
-// Whether the weights are read once: 8 rows a group at most on average, so that
-// few groups have a second unit, and 96 MiB of them or more, which the caches do not
-// keep between calls beside everything else.  4096 x 2048 gated, through the
-// caches and past them: 64 experts (285 MB), 1 row a group on average 33.4 and
-// 31.0 us, 4 rows 47.1 and 45.0, 8 rows 50.5 and 48.1, 16 rows 57.8 and 61.2; 16
-// experts (71 MB) 13.6 and 13.8.
+// Whether the weights go past the caches: 8 rows a group at most on average, so
+// that few groups have a second unit, and matrices of 96 MiB or more in all,
+// which the caches do not keep until a later call wants the same ones, beside
+// everything else.  It goes by all of them, also where there are fewer rows than
+// groups.  Both launches, 4096 x 2048 gated (4 MiB of codes a matrix), weights that
+// other calls' have displaced, through the caches and past them: 64 experts with
+// a row each 53.6 and 49.8 us, 4 rows 54.4 and 50.6, 8 rows 55.6 and 51.9, 16 rows
+// 57.8 and 61.2; 512 rows of which one expert has 449 64.5 and 63.8; 8 rows of 8 of
+// them 12.5 and 11.9, 23 of 23 24.2 and 22.7.  Where nothing came in between, 64
+// groups of 4 rows 48.5 and 50.2, 512 rows with one of 449 58.9 and 63.9, 8 rows
+// 10.7 to 11.5 and 10.4 to 11.7 by the run.
 static bool read_once(const GroupedArgs &a) {
   return a.R / least(a.E, a.R) <= 8 && (int64_t)a.E * a.N * (a.K / 2) >= (int64_t)96 << 20;
 }
@@ -287,11 +292,11 @@ static hipError_t run_tile(const GroupedArgs &a, hipStream_t stream) {
 }
 
 // Whether the 128-row tiles are the faster form: groups of 32 rows on average
-// and a tile for every CU.  Both timed, 16-row units against tiles: 2048 rows of
-// 64 experts, 2048 x 1024: 18.5 and 16.9 us; 4096 rows, 4096 x 2048: 98 and 72.
-// Below either bound: 1280 rows (20 a group) of 4096 x 1024 31.8 and 34.5; 256
-// rows of 8 experts, 4096 x 2048 (128 tiles) 9.9 and 12.1.  The tiles also need
-// their pairs of column groups whole.
+// and a tile for every CU.  Both timed on groups of one size, 16-row units
+// against tiles: 2048 rows of 64 experts, 2048 x 1024: 18.5 and 16.9 us; 4096
+// rows, 4096 x 2048: 98 and 72.  Below either bound: 1280 rows (20 a group) of 4096
+// x 1024 31.8 and 34.5; 256 rows of 8 experts, 4096 x 2048 (128 tiles) 9.9 and
+// 12.1.  The tiles also need their pairs of column groups whole.
 static bool use_tiles(const GroupedArgs &a) {
   const int64_t some = least(a.E, a.R);
   const int64_t units = a.R / 128 > some ? a.R / 128 : some;

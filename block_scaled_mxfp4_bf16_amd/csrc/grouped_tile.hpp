@@ -16,7 +16,9 @@
 //
 // What a CU takes in bounds it: 48 KiB a K step for its two tiles in 0.93 us, of
 // which the matrix units work 0.43.  32768 rows of 64 experts, 4096 x 2048 gated:
-// 166 us, 3.3 PFLOP/s; 2048 x 2048: 91 us, 3.0 PFLOP/s.
+// 173 us, 3.2 PFLOP/s (a call among others less its packing; under the profiler,
+// between whose launches the clocks move, medians of 183 to 207 and 160 at least);
+// 2048 x 2048: 96 us, 2.9 PFLOP/s (medians 100 to 105, least 92).
 #pragma once
 
 #include <type_traits>
@@ -207,8 +209,8 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(const GroupedArgs 
     // lower half in j = 2 p + 1 leaves each lane eight neighbouring columns, 16
     // bytes.  Stored as they lie, two lanes of a row would write 32 bytes of
     // it; through LDS, 32 rows at a time, a store covers all of the wave's
-    // columns of a row (32768 rows of 64 experts, 2048 x 2048: 102 us without,
-    // 91 with it; 4096 x 2048 gated, half the columns: 169 and 166).
+    // columns of a row (32768 rows of 64 experts, least times: 2048 x 2048 102 us
+    // without, 91 with it; 4096 x 2048 gated, half the columns: 169 and 166).
     // The lane number is found anew for each tile, from a zero that the
     // compiler cannot see through: it would keep the offsets of every store
     // through the products otherwise, and has no registers for them.

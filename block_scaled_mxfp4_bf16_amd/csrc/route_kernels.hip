@@ -18,8 +18,8 @@
 // computed in f64, one lane each, and rounded once.
 //
 // The k maxima depend on each other, and that chain bounds it, not memory: 8192
-// tokens of 128 experts, sigmoid with a bias, k 8, take 11.1 us to choose (4 MB of
-// logits) and 6.6 to place; one token of 64 experts 5.0 us, one launch.
+// tokens of 128 experts, sigmoid with a bias, k 8, take 11.6 us to choose (4 MB of
+// logits; least 10.9) and 6.8 to place; one token of 64 experts 5.2 us, one launch.
 #include <type_traits>
 
 #include "experts_bounds.hpp"
@@ -122,9 +122,18 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int l
   const double total = softmax && !a.renorm ? sum64() : 1.0;
 
   // Without a bias the key is the logit's own.  With one it is that of an f32
-  // estimate of g + bias, off by less than `slack` / 2: the exponential and
-  // quotient of g by less than 2^-21, the sum of E <= 1024 terms in a softmax
-  // by less than 2^-19 of g <= 1, the addition by 2^-24 of the result.
+  // estimate of g + bias.  Two of them are out of order only where they are
+  // closer than 2^-18 + 2^-22 of the larger, which is what decides below whether
+  // f64 is asked: the addition is off by 2^-24 of its result, and g by less than
+  // 2^-19 = 32 u, u = 2^-24 (hardware exponential and reciprocal: 1 ulp, 2 u).
+  //   sigmoid  e = exp(-x) is off by (1.5 |x| + 2) u e; g (1 - g) of that, at most
+  //            0.9 u, 1 + e rounds once and the reciprocal: 4 u together.
+  //   softmax  g = exp(d) / s, d = x - top <= 0.  Its own exponential: (2.5 |d| +
+  //            2) u g with |d| exp(d) < 0.37, the reciprocal 2 u, the product 1 u,
+  //            the sum's V - 1 + log2(L) <= 21 additions 21 u g.  The exponentials
+  //            summed add (2 + 2.5 a) u g, a = sum of g |d|, which is at most
+  //            h(g) + (1 - g) ln 1024 (h the entropy of g and 1 - g): largest all
+  //            together near g = 1, where a is next to 0: below 29 u.
   uint32_t key[V];
   if constexpr (BIAS) {
     float g[V];

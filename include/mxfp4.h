@@ -304,11 +304,11 @@ typedef enum { MXFP4_TYPE_BF16 = 0, MXFP4_TYPE_F16 = 1, MXFP4_TYPE_F32 = 2 } mxf
 /* Products of a few rows with MXFP4 weights, the activations unquantized:   */
 /*   y[r, n] = sum_k x[r, k] * B[n, k]                 (ids == NULL)          */
 /*   y[r, n] = sum_k x[r / repeat, k] * B_ids[r][n, k]  (ids != NULL)         */
-/* The weights are exact, the sums f32 in an order that M, N, K and gated     */
-/* fix, rounded once to y's type.  Scale bytes 0 to 254 all count (weights up to 6 * 2^127); 255, which */
-/* stands for NaN, makes its columns of y NaN or infinite.  f32 rows count    */
-/* down to 2^-133.  Made for single tokens and small batches, whose time is that of    */
-/* reading B; any M is right.                                                */
+/* The weights are exact, the sums f32 in an order that M, N, K and gated    */
+/* fix, rounded once to y's type.  Scale bytes 0 to 254 all count (weights   */
+/* up to 6 * 2^127); 255, which stands for NaN, makes its columns of y NaN   */
+/* or infinite.  f32 rows count down to 2^-133.  Made for single tokens and  */
+/* small batches, whose time is that of reading B; any M is right.           */
 /*   x       rows of K elements of x_type, ldx elements apart       (input)   */
 /*   Bq_sh, Bs_sh  one prepared matrix, or `experts` of them        (input)   */
 /*   ids     int32 [M]: the matrix of each row; a row whose id is outside    */
