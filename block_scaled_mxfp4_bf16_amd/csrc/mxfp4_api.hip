@@ -324,7 +324,10 @@ bool choose(int M, int N, int K, Schedule *s, bool need_pq = false) {
   {
     std::lock_guard<std::mutex> lk(g_memo_mu);
     if (g_memo.size() >= 4096) g_memo.clear();
-    g_memo[key] = ChoiceMemo{ok, r};
+    try {
+      g_memo[key] = ChoiceMemo{ok, r};
+    } catch (...) {  // not remembered
+    }
   }
   if (ok) *s = r;
   return ok;
@@ -376,6 +379,17 @@ uint64_t thread_of(hipStream_t stream) {
 
 }  // namespace
 
+// No exception may leave a C entry: what the host's containers and locks throw
+// (out of memory, in effect) becomes a status.
+template <class F>
+mxfp4_status_t no_throw(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return hip_status(hipErrorOutOfMemory);
+  }
+}
+
 namespace mxfp4 {
 
 mxfp4_status_t ready_workspace(size_t need, hipStream_t stream) {
@@ -383,14 +397,16 @@ mxfp4_status_t ready_workspace(size_t need, hipStream_t stream) {
   int dev = 0;
   if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
   void *p = nullptr;
-  return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, &p, thread_of(stream));
+  return no_throw([&] { return (mxfp4_status_t)g_ws.get(dev, (void *)stream, need, &p, thread_of(stream)); });
 }
 
 mxfp4_status_t hold_workspace(size_t need, hipStream_t stream, HeldWorkspace *out) {
   if (need == 0) return MXFP4_OK;
   int dev = 0;
   if (hipError_t e0 = hipGetDevice(&dev); e0 != hipSuccess) return hip_status(e0);
-  return (mxfp4_status_t)g_ws.hold(dev, (void *)stream, need, &out->ptr, &out->lock, thread_of(stream));
+  return no_throw([&] {
+    return (mxfp4_status_t)g_ws.hold(dev, (void *)stream, need, &out->ptr, &out->lock, thread_of(stream));
+  });
 }
 
 }  // namespace mxfp4

@@ -101,6 +101,7 @@ class WorkspacePool {
       if (e.device != device || e.stream != stream || e.thread != thread) continue;
       if (e.bytes < need) {
         size_t bytes = e.bytes * 2 > need ? e.bytes * 2 : need;
+        retired_.reserve(retired_.size() + 1);  // what throws comes before the buffer
         void *p = nullptr;
         if (int st = alloc_(device, stream, bytes, &p)) return st;
         retired_.push_back(e);
@@ -111,9 +112,11 @@ class WorkspacePool {
       *busy = e.busy;
       return 0;
     }
+    live_.reserve(live_.size() + 1);
+    auto mutex = std::make_shared<std::mutex>();
     void *p = nullptr;
     if (int st = alloc_(device, stream, need, &p)) return st;
-    live_.push_back(Entry{device, stream, thread, p, need, std::make_shared<std::mutex>()});
+    live_.push_back(Entry{device, stream, thread, p, need, std::move(mutex)});
     *out = p;
     *busy = live_.back().busy;
     return 0;

@@ -41,6 +41,10 @@ def test_launches_of_two_calls_do_not_mix(check, what):
     run(check, what)
 
 
+def test_no_exception_leaves_a_c_entry(check):
+    run(check, "no_host_memory")
+
+
 def test_no_data_race(tmp_path):
     probe = subprocess.run(["g++", "-fsanitize=thread", "-x", "c++", "-", "-o", str(tmp_path / "t")],
                            input="int main(){return 0;}", capture_output=True, text=True)

@@ -15,6 +15,7 @@
 #include <condition_variable>
 #include <map>
 #include <mutex>
+#include <new>
 #include <set>
 #include <thread>
 #include <vector>
@@ -52,6 +53,17 @@ static hipError_t two_launches(void *base) {
   return hipSuccess;
 }
 
+// ---- host memory that runs out ----
+static std::atomic<bool> g_no_memory{false};
+static std::atomic<int> g_device_buffers{0};
+void *operator new(size_t n) {
+  void *p = g_no_memory ? nullptr : malloc(n ? n : 1);
+  if (!p) throw std::bad_alloc();
+  return p;
+}
+void operator delete(void *p) noexcept { free(p); }
+void operator delete(void *p, size_t) noexcept { free(p); }
+
 // ---- HIP ----
 extern "C" {
 hipError_t hipGetDevice(int *d) {
@@ -59,6 +71,7 @@ hipError_t hipGetDevice(int *d) {
   return hipSuccess;
 }
 hipError_t hipMalloc(void **p, size_t n) {
+  ++g_device_buffers;
   *p = aligned_alloc(256, (n + 255) & ~(size_t)255);
   return hipSuccess;
 }
@@ -147,8 +160,20 @@ int main(int argc, char **argv) {
     }
     CHECK(n == all.size());
     CHECK(mxfp4_reserve_bytes(1000, hipStreamPerThread) == MXFP4_OK);
+  } else if (!strcmp(what, "no_host_memory")) {
+    // a status, not an exception through the C entry; no device buffer that nothing remembers
+    CHECK(call(2, 1, (void *)0x40) == MXFP4_OK);  // the schedule of this shape is remembered
+    for (int which : {0, 1, 2}) {
+      const int before = g_device_buffers;
+      g_no_memory = true;
+      const int st = call(which, 1, (void *)0x80);
+      const int reserved = mxfp4_reserve_bytes(1000, (void *)0x80);
+      g_no_memory = false;
+      CHECK(st == MXFP4_ERR_HIP && reserved == MXFP4_ERR_HIP && g_device_buffers == before);
+    }
+    for (int which : {0, 1, 2}) CHECK(call(which, 1, (void *)0x80) == MXFP4_OK);
   } else {
-    fprintf(stderr, "one_stream, two_streams or stream_per_thread\n");
+    fprintf(stderr, "one_stream, two_streams, stream_per_thread or no_host_memory\n");
     return 2;
   }
   printf("%s ok\n", what);
