@@ -302,7 +302,7 @@ def _exact_act(act, z):
         s = torch.special.expit(z)
         return z * s, s * (1 + z * torch.special.expit(-z))
     if act == "gelu":
-        p = torch.special.ndtr(z)
+        p = 0.5 * torch.erfc(z * -math.sqrt(0.5))
         return z * p, p + z * torch.exp(-z.square() / 2) / math.sqrt(2 * math.pi)
     t = torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z.pow(3)))
     du = math.sqrt(2 / math.pi) * (1 + 0.134145 * z.square())
