@@ -69,6 +69,14 @@ def _load():
         "mxfp4_gemm_grouped_workspace_bytes": (SZ, [I64, I64, I64]),
         "mxfp4_gemm_grouped": (I, [P, I64, I64, P, P, I64, P, P, I64, P, I64, I64, I64, I64, I, P, SZ, P]),
         "mxfp4_moe_combine": (I, [P, I, I64, I64, P, P, P, I64, P, I, I64, I64, I64, I64, P]),
+        "mxfp4_linear_workspace_bytes": (SZ, [I64, I64, I64]),
+        "mxfp4_linear": (I, [P, I64, P, P, P, I, I, I, P, I64, P, I, I64, P, I64, I64, I64, I64, P, SZ, P]),
+        "mxfp4_linear_grad_pre_workspace_bytes": (SZ, [I64, I64]),
+        "mxfp4_linear_grad_pre": (I, [P, I, I64, P, I64, I, I, P, I64, P, I64, I64, P, SZ, P]),
+        "mxfp4_linear_grad_input_workspace_bytes": (SZ, [I64, I64, I64]),
+        "mxfp4_linear_grad_input": (I, [P, I64, P, P, P, I, I64, I64, I64, I64, P, SZ, P]),
+        "mxfp4_linear_grad_weight_workspace_bytes": (SZ, [I64, I64, I64]),
+        "mxfp4_linear_grad_weight": (I, [P, I64, P, I64, P, I, I64, I64, I64, I64, P, SZ, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -89,7 +97,10 @@ def exported_symbols():
             "mxfp4_gemm_ex", "mxfp4_gemm_noalloc", "mxfp4_gemm_q", "mxfp4_gemm_q_schedule_name", "mxfp4_reserve", "mxfp4_status_string", "mxfp4_last_hip_error", "mxfp4_gemm_schedule_name",
             "mxfp4_set_quant_mode", "mxfp4_set_schedule_override", "mxfp4_list_schedules",
             "mxfp4_gemv", "mxfp4_reserve_bytes", "mxfp4_moe_route_workspace_bytes", "mxfp4_moe_route",
-            "mxfp4_gemm_grouped_workspace_bytes", "mxfp4_gemm_grouped", "mxfp4_moe_combine"]
+            "mxfp4_gemm_grouped_workspace_bytes", "mxfp4_gemm_grouped", "mxfp4_moe_combine",
+            "mxfp4_linear_workspace_bytes", "mxfp4_linear", "mxfp4_linear_grad_pre_workspace_bytes",
+            "mxfp4_linear_grad_pre", "mxfp4_linear_grad_input_workspace_bytes", "mxfp4_linear_grad_input",
+            "mxfp4_linear_grad_weight_workspace_bytes", "mxfp4_linear_grad_weight"]
 
 
 def _check(rc: int, what: str):
@@ -263,6 +274,50 @@ def mxfp4_moe_combine(y, y_type: int, ld_y: int, rows: int, weights, pos, residu
                                      _ptr(out), out_type, ld_out, T, k, N, _stream(stream)), "mxfp4_moe_combine")
 
 
+def mxfp4_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _load().mxfp4_linear_workspace_bytes(M, N, K)
+
+
+def mxfp4_linear(x, ldx: int, Bq_sh, Bs_sh, bias, bias_type: int, activation: int, gated: bool, residual, ld_res: int,
+                 y, y_type: int, ldy: int, pre, ld_pre: int, M: int, N: int, K: int, workspace=None,
+                 workspace_bytes: int = 0, stream=None):
+    _check(_load().mxfp4_linear(_ptr(x), ldx, _ptr(Bq_sh), _ptr(Bs_sh), _ptr(bias), bias_type, activation,
+                                int(bool(gated)), _ptr(residual), ld_res, _ptr(y), y_type, ldy, _ptr(pre), ld_pre, M, N,
+                                K, _ptr(workspace), workspace_bytes, _stream(stream)), "mxfp4_linear")
+
+
+def mxfp4_linear_grad_pre_workspace_bytes(M: int, N: int) -> int:
+    return _load().mxfp4_linear_grad_pre_workspace_bytes(M, N)
+
+
+def mxfp4_linear_grad_pre(dy, dy_type: int, ld_dy: int, pre, ld_pre: int, activation: int, gated: bool, dz, ld_dz: int,
+                          dbias, M: int, N: int, workspace=None, workspace_bytes: int = 0, stream=None):
+    _check(_load().mxfp4_linear_grad_pre(_ptr(dy), dy_type, ld_dy, _ptr(pre), ld_pre, activation, int(bool(gated)),
+                                         _ptr(dz), ld_dz, _ptr(dbias), M, N, _ptr(workspace), workspace_bytes,
+                                         _stream(stream)), "mxfp4_linear_grad_pre")
+
+
+def mxfp4_linear_grad_input_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _load().mxfp4_linear_grad_input_workspace_bytes(M, N, K)
+
+
+def mxfp4_linear_grad_input(dz, ld_dz: int, Bq_sh, Bs_sh, dx, dx_type: int, ld_dx: int, M: int, N: int, K: int,
+                            workspace=None, workspace_bytes: int = 0, stream=None):
+    _check(_load().mxfp4_linear_grad_input(_ptr(dz), ld_dz, _ptr(Bq_sh), _ptr(Bs_sh), _ptr(dx), dx_type, ld_dx, M, N, K,
+                                           _ptr(workspace), workspace_bytes, _stream(stream)), "mxfp4_linear_grad_input")
+
+
+def mxfp4_linear_grad_weight_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _load().mxfp4_linear_grad_weight_workspace_bytes(M, N, K)
+
+
+def mxfp4_linear_grad_weight(dz, ld_dz: int, x, ldx: int, dw, dw_type: int, ld_dw: int, M: int, N: int, K: int,
+                             workspace=None, workspace_bytes: int = 0, stream=None):
+    _check(_load().mxfp4_linear_grad_weight(_ptr(dz), ld_dz, _ptr(x), ldx, _ptr(dw), dw_type, ld_dw, M, N, K,
+                                            _ptr(workspace), workspace_bytes, _stream(stream)),
+           "mxfp4_linear_grad_weight")
+
+
 # ---- tensor conveniences (allocate outputs with torch, then call the above) --
 
 def _allocator(stream):
@@ -417,11 +472,10 @@ def _rows_of(t, what, rows, cols, dev):
                      (what, rows, cols, _device(dev)))
 
 
-def _no_gradients(what):
+def _no_gradients(what, how="and the expert operators have none"):
     """For an input that requires gradients: refuses a call that autograd would follow."""
     if _torch.is_grad_enabled():
-        raise RuntimeError("%s requires gradients, and the expert operators have none: detach it, or call under "
-                           "torch.no_grad()" % what)
+        raise RuntimeError("%s requires gradients, %s: detach it, or call under torch.no_grad()" % (what, how))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -445,7 +499,7 @@ def _on_gpu(dev):
     """A launch goes to the current device; tensors of another would be read from there."""
     global _current_device
     if dev < 0:
-        raise ValueError("the expert operators take cuda tensors")
+        raise ValueError("the operators take cuda tensors")
     if _current_device is None:
         import torch
         _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -662,4 +716,187 @@ def moe_combine(y, weights, pos=None, residual=None, out=None, out_dtype=None, s
                                    ld_out, T, k, N, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_moe_combine")
+    return out
+
+
+# ---- dense layers --------------------------------------------------------------
+
+MXFP4_ACT_NONE, MXFP4_ACT_RELU, MXFP4_ACT_SILU, MXFP4_ACT_GELU, MXFP4_ACT_GELU_TANH = range(5)
+
+_activations = {None: MXFP4_ACT_NONE, "none": MXFP4_ACT_NONE, "relu": MXFP4_ACT_RELU, "silu": MXFP4_ACT_SILU,
+                "gelu": MXFP4_ACT_GELU, "gelu_tanh": MXFP4_ACT_GELU_TANH}
+
+
+def _activation(name):
+    kind = _activations.get(name)
+    if kind is None:
+        raise ValueError("activation must be None, 'none', 'relu', 'silu', 'gelu' or 'gelu_tanh', not %r" % (name,))
+    return kind
+
+
+def _untracked(t, what):
+    if t.requires_grad:
+        _no_gradients(what, "which autograd does not follow through this call (mx.linear_grad_* compute them)")
+
+
+def _bf16(t, what):
+    if t.dtype is not _torch.bfloat16:
+        raise TypeError("%s must be bf16, not %s" % (what, t.dtype))
+
+
+def _output(out, rows, cols, dtype, like, dev, stream):
+    """The output tensor, its MXFP4_TYPE_* and its row stride."""
+    if out is None:
+        out = (_torch.empty if stream is None else _allocator(stream))((rows, cols), dtype=dtype, device=like.device)
+        return out, _type(out), cols
+    return out, _type(out), _rows_of(out, "out", rows, cols, dev)
+
+
+def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, residual=None, pre=None, out=None,
+           out_dtype=None, stream=None, workspace=None):
+    """A dense layer: z = Q(x) * B^T + bias, y = f(z) + residual.
+
+    x [M, K] bf16 with contiguous rows; Bw, Bs from prepare_b; bias [N], bf16,
+    f16 or f32; activation f None, "relu", "silu", "gelu" or "gelu_tanh" (of the
+    f32 z); residual [M, columns] of y's type, which may be out itself.
+    gated: y = f(z's first half) * z's second half + residual, N/2 columns.
+    y's type is out's, else out_dtype, else residual's, else bf16.
+
+    pre: a bf16 [M, N] tensor that receives z, or True for a new one; the call
+    then returns (y, z), and linear_grad_pre takes z.
+    workspace: as for gemm_grouped, of mxfp4_linear_workspace_bytes(M, N, K) bytes."""
+    L = _lib if _torch else _start()
+    torch = _torch
+    ws, ws_bytes = None, 0
+    M, K, ldx, dev = _matrix(x, "x", "M, K")
+    _bf16(x, "x")
+    _untracked(x, "x")
+    kind = _activation(activation)
+    if _prepared(Bw, Bs, N, K, dev) != 1:
+        raise ValueError("Bw and Bs must hold one matrix")
+    cols = N // 2 if gated else N
+    bias_type = 0
+    if bias is not None:
+        bias_type = _type(bias)
+        _array(bias, bias.dtype, "bias", N, dev)
+        _untracked(bias, "bias")
+        bias = bias.data_ptr()
+    out, yt, ldy = _output(out, M, cols, out_dtype or (torch.bfloat16 if residual is None else residual.dtype), x, dev,
+                           stream)
+    ld_res = cols
+    if residual is not None:
+        ld_res = _rows_of(residual, "residual", M, cols, dev)
+        if residual.dtype != out.dtype:
+            raise TypeError("residual is %s, out %s" % (residual.dtype, out.dtype))
+        _untracked(residual, "residual")
+        residual = residual.data_ptr()
+    z, ld_pre = None, N
+    if pre is True:
+        pre = (torch.empty if stream is None else _allocator(stream))((M, N), dtype=torch.bfloat16, device=x.device)
+    if pre is not None and pre is not False:
+        _bf16(pre, "pre")
+        ld_pre = _rows_of(pre, "pre", M, N, dev)
+        z = pre.data_ptr()
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace, dev)
+    _on_gpu(dev)
+    rc = L.mxfp4_linear(x.data_ptr(), ldx, Bw.data_ptr(), Bs.data_ptr(), bias, bias_type, kind, 1 if gated else 0,
+                        residual, ld_res, out.data_ptr(), yt, ldy, z, ld_pre, M, N, K, ws, ws_bytes,
+                        _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_linear")
+    return out if z is None and not isinstance(pre, torch.Tensor) else (out, pre)
+
+
+def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias: bool = False, out=None, stream=None,
+                    workspace=None):
+    """The gradient of z in linear, bf16 [M, N], from that of y.
+
+    dy [M, columns of y], bf16, f16 or f32, with contiguous rows; pre the z
+    that linear kept (None where it has neither activation nor gate, when z is
+    not read).  bias: returns (dz, dbias), dbias f32 [N] the sum of the rows of
+    dz, formed before dz is rounded.  out may be pre itself.
+    workspace: as for gemm_grouped, of mxfp4_linear_grad_pre_workspace_bytes(M, N)
+    bytes; without bias none is needed."""
+    L = _lib if _torch else _start()
+    torch = _torch
+    ws, ws_bytes = None, 0
+    M, cols, ld_dy, dev = _matrix(dy, "dy", "M, columns")
+    dt = _type(dy)
+    _untracked(dy, "dy")
+    kind = _activation(activation)
+    N = 2 * cols if gated else cols
+    z, ld_pre = None, N
+    if pre is not None:
+        _bf16(pre, "pre")
+        ld_pre = _rows_of(pre, "pre", M, N, dev)
+        _untracked(pre, "pre")
+        z = pre.data_ptr()
+    elif kind or gated:
+        raise ValueError("an activation or a gate needs pre")
+    if out is not None:
+        _bf16(out, "out")
+    out, _, ld_dz = _output(out, M, N, torch.bfloat16, dy, dev, stream)
+    db = None
+    if bias:
+        db = (torch.empty if stream is None else _allocator(stream))((N,), dtype=torch.float32, device=dy.device)
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace, dev)
+    _on_gpu(dev)
+    rc = L.mxfp4_linear_grad_pre(dy.data_ptr(), dt, ld_dy, z, ld_pre, kind, 1 if gated else 0, out.data_ptr(), ld_dz,
+                                 None if db is None else db.data_ptr(), M, N, ws, ws_bytes,
+                                 _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_linear_grad_pre")
+    return (out, db) if bias else out
+
+
+def linear_grad_input(dz, Bw, Bs, K: int, out=None, out_dtype=None, stream=None, workspace=None):
+    """The gradient of x in linear: dx = dz * B, [M, K].
+
+    dz [M, N] bf16 with contiguous rows; Bw, Bs the prepared [N, K] matrix.
+    dx's type is out's, else out_dtype, else bf16.
+    workspace: as for gemm_grouped, of mxfp4_linear_grad_input_workspace_bytes(M, N, K) bytes."""
+    L = _lib if _torch else _start()
+    ws, ws_bytes = None, 0
+    M, N, ld_dz, dev = _matrix(dz, "dz", "M, N")
+    _bf16(dz, "dz")
+    _untracked(dz, "dz")
+    if _prepared(Bw, Bs, N, K, dev) != 1:
+        raise ValueError("Bw and Bs must hold one matrix")
+    out, xt, ld_dx = _output(out, M, K, out_dtype or _torch.bfloat16, dz, dev, stream)
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace, dev)
+    _on_gpu(dev)
+    rc = L.mxfp4_linear_grad_input(dz.data_ptr(), ld_dz, Bw.data_ptr(), Bs.data_ptr(), out.data_ptr(), xt, ld_dx, M, N, K,
+                                   ws, ws_bytes, _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_linear_grad_input")
+    return out
+
+
+def linear_grad_weight(dz, x, out=None, out_dtype=None, stream=None, workspace=None):
+    """The gradient of the weights in linear: dw = dz^T * Q(x), [N, K].
+
+    dz [M, N] and x [M, K] bf16 with contiguous rows.  dw's type is out's, else
+    out_dtype, else f32.
+    workspace: as for gemm_grouped, of mxfp4_linear_grad_weight_workspace_bytes(M, N, K) bytes."""
+    L = _lib if _torch else _start()
+    ws, ws_bytes = None, 0
+    M, N, ld_dz, dev = _matrix(dz, "dz", "M, N")
+    _bf16(dz, "dz")
+    _untracked(dz, "dz")
+    rows, K, ldx, x_dev = _matrix(x, "x", "M, K")
+    if rows != M or x_dev != dev:
+        raise ValueError("x must have dz's %d rows on %s" % (M, _device(dev)))
+    _bf16(x, "x")
+    _untracked(x, "x")
+    out, wt, ld_dw = _output(out, N, K, out_dtype or _torch.float32, dz, dev, stream)
+    if workspace is not None:
+        ws, ws_bytes = _workspace(workspace, dev)
+    _on_gpu(dev)
+    rc = L.mxfp4_linear_grad_weight(dz.data_ptr(), ld_dz, x.data_ptr(), ldx, out.data_ptr(), wt, ld_dw, M, N, K, ws,
+                                    ws_bytes, _current_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "mxfp4_linear_grad_weight")
     return out

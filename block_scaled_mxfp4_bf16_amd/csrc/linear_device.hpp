@@ -1,0 +1,134 @@
+// Activations of the dense layer, their slopes, and vectors of a runtime type.
+#pragma once
+
+#include "experts_device.hpp"
+
+namespace mxfp4 {
+
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+// 1 / (1 + exp(-v)).  exp overflows to infinity below -88, where the
+// reciprocal is the right 0.
+__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+
+// The lower tail of the normal distribution at -|z|, and exp(-z^2 / 2).
+//   Phi(-|z|) = exp(-z^2 / 2) * erfcx(|z| / sqrt 2) / 2
+// with erfcx(a) as t * P(t), t = 1 / (1 + 0.4 a): least squares with Lawson's
+// weights on [0, 11], relative error 7e-8; past 11 the exponential is 0 in f32.
+// In this form the tail keeps its relative precision, which 1 + erf does not.
+__device__ __forceinline__ float normal_tail(float z, float &e) {
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.282842712f * __builtin_fabsf(z));
+  e = __expf(-0.5f * z * z);
+  float p = 0.04288044f;
+  p = p * t - 0.14825743f;
+  p = p * t + 0.1004372f;
+  p = p * t + 0.06910221f;
+  p = p * t + 0.09280704f;
+  p = p * t + 0.187831f;
+  p = p * t + 0.2033094f;
+  p = p * t + 0.22624436f;
+  p = p * t + 0.22564584f;
+  return 0.5f * e * t * p;
+}
+
+// gelu_tanh(z) = z * sigmoid(2 u), u = sqrt(2 / pi) * (z + 0.044715 z^3).  Past
+// 30 the sigmoid is 0 or 1, and its cube would overflow first.
+constexpr float kTanhC = 1.59576912f, kTanhC3 = 0.0713548163f;  // 2 sqrt(2 / pi), times 0.044715
+__device__ __forceinline__ float tanh_clamp(float z) { return __builtin_fminf(__builtin_fmaxf(z, -30.f), 30.f); }
+
+__device__ __forceinline__ float activate(int act, float z) {
+  if (act == kActRelu) return z < 0.f ? 0.f : z;
+  if (act == kActSilu) return z * sigmoid(z);
+  if (act == kActGelu) {
+    float e;
+    const float tail = normal_tail(z, e);
+    return z * (z < 0.f ? tail : 1.0f - tail);
+  }
+  if (act == kActGeluTanh) {
+    const float c = tanh_clamp(z);
+    return z * sigmoid(c * (kTanhC + kTanhC3 * c * c));
+  }
+  return z;
+}
+
+// f(z) and f'(z).
+__device__ __forceinline__ float activate_slope(int act, float z, float &slope) {
+  if (act == kActRelu) {
+    slope = z > 0.f ? 1.f : 0.f;
+    return z < 0.f ? 0.f : z;
+  }
+  if (act == kActSilu) {
+    const float s = sigmoid(z);
+    slope = s + z * s * (1.0f - s);
+    return z * s;
+  }
+  if (act == kActGelu) {
+    float e;
+    const float tail = normal_tail(z, e);
+    const float phi = z < 0.f ? tail : 1.0f - tail;
+    slope = phi + 0.398942280f * z * e;
+    return z * phi;
+  }
+  if (act == kActGeluTanh) {
+    const float c = tanh_clamp(z);
+    const float s = sigmoid(c * (kTanhC + kTanhC3 * c * c));
+    slope = s + z * s * (1.0f - s) * (kTanhC + 3.f * kTanhC3 * c * c);
+    return z * s;
+  }
+  slope = 1.f;
+  return z;
+}
+
+// Four neighbouring elements of an array of a runtime type (MXFP4_TYPE_*), in
+// one access where `wide` says that they are aligned to it.
+__device__ __forceinline__ v4f load4(const void *p, int type, int64_t i, int wide) {
+  v4f v;
+  if (type == 2) {
+    const float *f = (const float *)p + i;
+    if (wide) return *(const v4f *)f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = f[j];
+    return v;
+  }
+  const uint16_t *h = (const uint16_t *)p + i;
+  uint16_t d[4];
+  if (wide) {
+    const u32x2 w = *(const u32x2 *)h;
+    d[0] = (uint16_t)w.x, d[1] = (uint16_t)(w.x >> 16), d[2] = (uint16_t)w.y, d[3] = (uint16_t)(w.y >> 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = h[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = type == 0 ? __uint_as_float((uint32_t)d[j] << 16) : (float)__builtin_bit_cast(_Float16, d[j]);
+  return v;
+}
+
+// Two f32 -> two bf16, f16 in one dword, to nearest even.
+__device__ __forceinline__ uint32_t f16x2_rne(float a, float b) {
+  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+__device__ __forceinline__ void store4(void *p, int type, int64_t i, const v4f &v, int wide) {
+  if (type == 2) {
+    float *f = (float *)p + i;
+    if (wide) {
+      *(v4f *)f = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = v[j];
+    }
+    return;
+  }
+  const u32x2 d = type == 0 ? u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])}
+                            : u32x2{f16x2_rne(v[0], v[1]), f16x2_rne(v[2], v[3])};
+  uint16_t *h = (uint16_t *)p + i;
+  if (wide) {
+    *(u32x2 *)h = d;
+  } else {
+    h[0] = (uint16_t)d.x, h[1] = (uint16_t)(d.x >> 16), h[2] = (uint16_t)d.y, h[3] = (uint16_t)(d.y >> 16);
+  }
+}
+
+}  // namespace mxfp4

@@ -1,0 +1,172 @@
+// The dense layer on MXFP4 weights:
+//   z = Q(x) * B^T + bias,  y = f(z) + residual,
+// or, gated, y = f(first half of z's columns) * second half + residual.
+//
+// The rows are quantized into the prepared layout by a launch of their own,
+// so that both operands of the product are read as whole blocks.
+#include "linear_epilogue.hpp"
+#include "linear_internal.hpp"
+
+namespace mxfp4 {
+
+// Quantize rows into the prepared layout.  One wave takes one K step of 16
+// rows, as prepare_b does; four lanes share a group of 32 elements.  Rows past
+// the last one and groups past K become zero codes; scale bytes of rows and
+// groups that do not exist are written only where a product reads them with
+// the others of their dword, and meet zero codes.
+template <bool SW>
+__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t *x, int64_t ld, int rows, int K, uint8_t *codes,
+                                                        uint8_t *scales, int steps, int units) {
+  const int lane = threadIdx.x & 63;
+  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= units) return;
+  const int g = unit / steps, s = unit - g * steps;
+  const int G = K >> 5, gp = (G + 7) & ~7;
+  const int row = 16 * g + (lane >> 2);
+  const bool live = row < rows;
+  const uint16_t *from = x + (int64_t)(live ? row : 0) * ld + (lane & 3) * 8;
+  u32x4 w[4];
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    w[ch] = u32x4{0, 0, 0, 0};
+    if (live && 4 * s + ch < G) w[ch] = *(const u32x4 *)(from + (4 * s + ch) * 32);
+  }
+  uint32_t *to = (uint32_t *)(codes + (int64_t)g * K * 8);
+  uint8_t *block = scales + (int64_t)(row >> 5) * 32 * gp;
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    const int grp = 4 * s + ch;
+    uint32_t sc;
+    const uint32_t d = quant_quarter_t<SW>(w[ch], &sc);
+    if (grp < G) to[grp * 64 + lane] = d;
+    if ((lane & 3) == 0 && grp < gp) block[shuffled_scale_offset(row & 31, grp, gp)] = (uint8_t)sc;
+  }
+}
+
+hipError_t launch_pack_rows(const uint16_t *x, int64_t ld, int64_t rows, int64_t K, uint8_t *codes, uint8_t *scales,
+                            bool sw, hipStream_t stream) {
+  const int steps = (int)((K + 127) / 128);
+  const int64_t units = (rows + 15) / 16 * steps;
+  const unsigned blocks = (unsigned)((units + 3) / 4);
+  if (sw)
+    pack_rows_kernel<true><<<blocks, 256, 0, stream>>>(x, ld, (int)rows, (int)K, codes, scales, steps, (int)units);
+  else
+    pack_rows_kernel<false><<<blocks, 256, 0, stream>>>(x, ld, (int)rows, (int)K, codes, scales, steps, (int)units);
+  return hipGetLastError();
+}
+
+// 16 * MW rows x 16 * NT weight rows a workgroup; the WK waves take every
+// WK-th K step, hold the whole tile's sums and add them through LDS in wave
+// order.  Nothing waits at a barrier before that.  The weights are the first
+// operand of the instruction, so a lane holds four neighbouring columns of a
+// row.  Gated: the first NT / 2 weight groups are gate columns, the others
+// their up columns.
+template <int MW, int NT, int WK>
+__global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs a, int n_tiles) {
+  __shared__ __attribute__((aligned(16))) v4f red[WK][MW * NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m_tile = blockIdx.x / n_tiles, n_tile = blockIdx.x - m_tile * n_tiles;
+  const int K = a.K, N = a.N;
+  const int KS = (K + 127) >> 7;
+  const int gp = ((K >> 5) + 7) & ~7;
+  const int groups = N >> 4;
+  const int row0 = m_tile * 16 * MW;
+  const int x_groups = (a.M + 15) >> 4, xg0 = m_tile * MW;
+  const int q4 = lane >> 4;
+
+  const int64_t b_bytes = (int64_t)groups * K * 8, s_bytes = (int64_t)((N + 255) >> 8) * 8 * gp * 32;
+  const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)a.Bw, 0, (int)b_bytes, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)a.Bs, 0, (int)s_bytes, kRsrcWord3);
+  const int own_groups = x_groups - xg0 < MW ? x_groups - xg0 : MW;
+  const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.codes + (int64_t)xg0 * K * 8), 0, own_groups * K * 8, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t xs_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(a.scales + (int64_t)(xg0 >> 1) * gp * 32), 0, (((xg0 & 1) + own_groups + 1) >> 1) * gp * 32, kRsrcWord3);
+
+  int gw[NT];
+  bool gok[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (a.gated) {
+      const int c = n_tile * (NT / 2) + nt % (NT / 2);
+      gok[nt] = c < (groups >> 1);
+      gw[nt] = nt < NT / 2 ? c : (groups >> 1) + c;
+    } else {
+      gw[nt] = n_tile * NT + nt;
+      gok[nt] = gw[nt] < groups;
+    }
+  }
+  v4f acc[MW][NT];
+#pragma unroll
+  for (int mt = 0; mt < MW; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  for (int ks = wave; ks < KS; ks += WK) {
+    // a K chunk past the end meets zeros of the rows; it must not run past
+    // the matrix all the same
+    const bool ok = (4 * ks + q4) * 32 < K;
+    u32x4 x[MW], b[NT];
+    uint32_t xs[MW], bs[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
+          b_rsrc, off_or_oob(ok && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
+      bs[nt] = __builtin_amdgcn_raw_buffer_load_b32(
+          s_rsrc, off_or_oob(gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MW; ++mt) {
+      x[mt] = __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, off_or_oob(ok, mt * K * 8 + ks * 1024 + lane * 16), 0, 0);
+      xs[mt] = __builtin_amdgcn_raw_buffer_load_b32(
+          xs_rsrc, (((xg0 & 1) + mt) >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4, 0, 0);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MW; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        acc[mt][nt] = mfma_fp4(b[nt], x[mt], acc[mt][nt], bs[nt] >> (8 * ((gw[nt] & 1) + 2 * (ks & 1))),
+                               xs[mt] >> (8 * (((xg0 + mt) & 1) + 2 * (ks & 1))));
+  }
+#pragma unroll
+  for (int mt = 0; mt < MW; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) red[wave][mt * NT + nt][lane] = acc[mt][nt];
+  __syncthreads();
+
+  const auto sum = [&](int block, int l) {
+    v4f v = red[0][block][l];
+#pragma unroll
+    for (int w = 1; w < WK; ++w) v += red[w][block][l];
+    return v;
+  };
+  const int blocks = a.gated ? MW * NT / 2 : MW * NT;
+  for (int j = threadIdx.x; j < blocks * 64; j += 64 * WK) {
+    const int l = j & 63, block = j >> 6;
+    const int across = a.gated ? NT / 2 : NT;
+    const int mt = block / across, nt = block - mt * across;
+    const int row = row0 + mt * 16 + (l & 15);
+    const int col = (n_tile * across + nt) * 16 + (l >> 4) * 4;
+    if (row >= a.M || col >= (a.gated ? N >> 1 : N)) continue;
+    const v4f z = sum(mt * NT + nt, l);
+    const v4f up = a.gated ? sum(mt * NT + nt + NT / 2, l) : z;
+    linear_emit(a, row, col, z, up);
+  }
+}
+
+size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return packed_bytes(M, K); }
+
+hipError_t launch_linear(LinearArgs a, hipStream_t stream) {
+  a.codes = a.ws;
+  a.scales = a.ws + (packed_codes_bytes(a.M, a.K) + 255) / 256 * 256;
+  const hipError_t e = launch_pack_rows(a.x, a.ldx, a.M, a.K, a.codes, a.scales, a.sw, stream);
+  if (e != hipSuccess) return e;
+  const int cols = a.gated ? a.N / 2 : a.N, width = a.gated ? 32 : 64;
+  const int n_tiles = (cols + width - 1) / width;
+  const int m_tiles = (a.M + 63) / 64;
+  linear_split_kernel<4, 4, 4><<<(unsigned)((int64_t)n_tiles * m_tiles), 256, 0, stream>>>(a, n_tiles);
+  return hipGetLastError();
+}
+
+}  // namespace mxfp4

@@ -427,6 +427,96 @@ MXFP4_API mxfp4_status_t mxfp4_moe_combine(const void *y, int y_type, int64_t ld
                                            int64_t ld_res, void *out, int out_type, int64_t ld_out, int64_t T,
                                            int64_t k, int64_t N, mxfp4_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Dense layers: the product with what surrounds it in a model, and its      */
+/* gradients.  With W the values of a matrix prepared as for mxfp4_gemm, Q   */
+/* the quantization of mxfp4_quantize and f an activation:                   */
+/*   z = Q(x) * W^T + bias                                                    */
+/*   y = f(z) + residual                                  (gated == 0)        */
+/*   y = f(z[:, :N/2]) * z[:, N/2:] + residual             (gated != 0: the    */
+/*       weight matrix holds the gate's rows first, y has N/2 columns)       */
+/* The gradients go through Q as if it were the identity.  What was said     */
+/* above of the expert operators' workspaces holds for these as well; a call */
+/* whose ..._workspace_bytes is 0 needs none.  Sums are f32 in an order that */
+/* the sizes of the call fix, so results are the same every time; every      */
+/* output is rounded once, to nearest even.                                   */
+/* Limits of all of them: UNSUPPORTED for K % 32 != 0, N % 16 != 0, gated    */
+/* with N % 32 != 0, M or N > 2^20, K > 2^17, a prepared matrix beyond 2^31   */
+/* bytes, a row stride > 2^20 elements.                                       */
+/* ------------------------------------------------------------------------ */
+typedef enum {
+    MXFP4_ACT_NONE = 0,
+    MXFP4_ACT_RELU = 1,
+    MXFP4_ACT_SILU = 2,     /* v / (1 + exp(-v))                                */
+    MXFP4_ACT_GELU = 3,     /* v * Phi(v), Phi the normal distribution           */
+    MXFP4_ACT_GELU_TANH = 4 /* v / 2 * (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+} mxfp4_activation_t;
+
+/* The layer.                                                                 */
+/*   x         [M, K] bf16, rows ldx elements apart                 (input)  */
+/*   Bq_sh, Bs_sh  the prepared matrix [N, K]                        (input)  */
+/*   bias      [N] of bias_type, or NULL                             (input)  */
+/*   residual  [M, y's columns] of y_type, ld_res apart, or NULL; may be y   */
+/*             itself                                                (input)  */
+/*   y         [M, N] (gated: [M, N/2]) of y_type, ldy apart        (output) */
+/*   pre       [M, N] bf16, ld_pre apart, or NULL: receives z, which the     */
+/*             gradient of the activation takes                     (output) */
+/* The activation takes the f32 z.  M may be 0.  x must be finite.            */
+/* Errors: INVALID_ARG (null, M < 0, N or K < 1, unknown type or activation, */
+/*         a row stride smaller than the row, x or its row stride not        */
+/*         16-byte aligned, B not 16-byte aligned, another pointer not        */
+/*         aligned to its type); UNSUPPORTED (above); WORKSPACE; HIP.          */
+MXFP4_API size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+MXFP4_API mxfp4_status_t mxfp4_linear(const void *x, int64_t ldx, const void *Bq_sh, const void *Bs_sh,
+                                      const void *bias, int bias_type, int activation, int gated,
+                                      const void *residual, int64_t ld_res, void *y, int y_type, int64_t ldy,
+                                      void *pre, int64_t ld_pre, int64_t M, int64_t N, int64_t K, void *workspace,
+                                      size_t workspace_bytes, mxfp4_stream_t stream);
+
+/* The gradient of z, and of the bias:                                        */
+/*   dz = dy * f'(pre)                                                        */
+/*   dz = [dy * up * f'(gate), dy * f(gate)], pre = [gate, up]    (gated)      */
+/*   dbias[n] = sum over the rows of dz[:, n], before dz is rounded           */
+/* The slope of relu at 0 is 0.                                               */
+/*   dy     [M, y's columns] of dy_type, ld_dy apart                (input)  */
+/*   pre    [M, N] bf16, ld_pre apart, as mxfp4_linear left it; not read, and */
+/*          may be NULL, for MXFP4_ACT_NONE without gate             (input)  */
+/*   dz     [M, N] bf16, ld_dz apart; may be pre itself             (output) */
+/*   dbias  f32 [N] or NULL                                         (output) */
+/* M may be 0: dbias is then zero.  The workspace serves dbias only.          */
+/* Errors: as mxfp4_linear.                                                    */
+MXFP4_API size_t mxfp4_linear_grad_pre_workspace_bytes(int64_t M, int64_t N);
+MXFP4_API mxfp4_status_t mxfp4_linear_grad_pre(const void *dy, int dy_type, int64_t ld_dy, const void *pre,
+                                               int64_t ld_pre, int activation, int gated, void *dz, int64_t ld_dz,
+                                               float *dbias, int64_t M, int64_t N, void *workspace,
+                                               size_t workspace_bytes, mxfp4_stream_t stream);
+
+/* The gradient of x: dx[m, k] = sum_n dz[m, n] * W[n, k].                     */
+/* W's values are exact (those of 2^128 and more, from scale bytes 253 and    */
+/* 254, count as infinite; scale byte 255 stands for NaN), dz is taken as it  */
+/* is, down to its subnormal values.  A row of NaN or Inf touches its own row  */
+/* of dx only.                                                                 */
+/*   dz  [M, N] bf16, ld_dz apart                                   (input)  */
+/*   Bq_sh, Bs_sh  the prepared matrix [N, K]                        (input)  */
+/*   dx  [M, K] of dx_type, ld_dx apart                             (output) */
+/* M may be 0.                                                                 */
+/* Errors: as mxfp4_linear (dz and its row stride 16-byte aligned).            */
+MXFP4_API size_t mxfp4_linear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K);
+MXFP4_API mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, const void *Bq_sh, const void *Bs_sh,
+                                                 void *dx, int dx_type, int64_t ld_dx, int64_t M, int64_t N,
+                                                 int64_t K, void *workspace, size_t workspace_bytes,
+                                                 mxfp4_stream_t stream);
+
+/* The gradient of W: dw[n, k] = sum_m dz[m, n] * Q(x)[m, k].                  */
+/*   dz  [M, N] bf16, ld_dz apart;  x  [M, K] bf16, ldx apart, finite (input) */
+/*   dw  [N, K] of dw_type, ld_dw apart                             (output) */
+/* M may be 0: dw is then zero.                                                */
+/* Errors: as mxfp4_linear (dz, x and their row strides 16-byte aligned).      */
+MXFP4_API size_t mxfp4_linear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K);
+MXFP4_API mxfp4_status_t mxfp4_linear_grad_weight(const void *dz, int64_t ld_dz, const void *x, int64_t ldx, void *dw,
+                                                  int dw_type, int64_t ld_dw, int64_t M, int64_t N, int64_t K,
+                                                  void *workspace, size_t workspace_bytes, mxfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
