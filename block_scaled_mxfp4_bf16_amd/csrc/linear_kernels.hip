@@ -15,7 +15,7 @@ namespace mxfp4 {
 // groups that do not exist are written only where a product reads them with
 // the others of their dword, and meet zero codes.
 template <bool SW>
-__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t *x, int64_t ld, int rows, int K, uint8_t *codes,
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const uint16_t *x, int64_t ld, int rows, int K, uint8_t *codes,
                                                         uint8_t *scales, int steps, int units) {
   const int lane = threadIdx.x & 63;
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -49,9 +49,9 @@ hipError_t launch_pack_rows(const uint16_t *x, int64_t ld, int64_t rows, int64_t
   const int64_t units = (rows + 15) / 16 * steps;
   const unsigned blocks = (unsigned)((units + 3) / 4);
   if (sw)
-    pack_rows_kernel<true><<<blocks, 256, 0, stream>>>(x, ld, (int)rows, (int)K, codes, scales, steps, (int)units);
+    quantize_rows_kernel<true><<<blocks, 256, 0, stream>>>(x, ld, (int)rows, (int)K, codes, scales, steps, (int)units);
   else
-    pack_rows_kernel<false><<<blocks, 256, 0, stream>>>(x, ld, (int)rows, (int)K, codes, scales, steps, (int)units);
+    quantize_rows_kernel<false><<<blocks, 256, 0, stream>>>(x, ld, (int)rows, (int)K, codes, scales, steps, (int)units);
   return hipGetLastError();
 }
 
