@@ -42,32 +42,39 @@ __device__ __forceinline__ u32x4 bf16_of_codes(uint32_t w, float scale) {
   return r;
 }
 
-// Place of 16-byte chunk c in row j of an LDS tile of `row_bytes` a row that is
-// written row by row and read turned: 8 rows' chunks c lie in other banks, and so
-// do the two chunks of 4 rows that a turned read takes.
+// Place of 16-byte chunk c in row j of an LDS tile of `row_bytes` a row (a
+// multiple of 256) that is written row by row and read turned.  LDS has 64 banks
+// of 4 bytes, a turned read takes 32 lanes at once, 64 bytes of each of 4 rows, and
+// a write 8 lanes, one chunk of each of 8 rows: either lies in banks of its own.
+// (With the 4 rows 32 bytes apart instead, every turned read took twice its
+// cycles.)
+__device__ __forceinline__ constexpr int turn_swizzle(int j) { return ((j & 3) << 2) | ((j >> 2) & 1); }
 __device__ __forceinline__ int turned_at(int j, int c, int row_bytes) {
-  return j * row_bytes + ((c ^ (((j & 3) << 1) | ((j >> 2) & 1))) << 4);
+  return j * row_bytes + ((c ^ turn_swizzle(j)) << 4);
 }
+// The same for rows of 128 bytes of which 16 lanes read chunk c of 16 rows.
+__device__ __forceinline__ constexpr int line_swizzle(int row) { return (row >> 1) & 7; }
 
-// BI x BK outputs a workgroup of 4 waves, WI of them along i; 64 of j a stage,
+// BI x BK outputs a workgroup of W waves, WI of them along i; 64 of j a stage,
 // taken in two halves of two 16-deep steps.
 //   P  goes through LDS as it is, written by the memory system: a ring of three
 //      stages, loaded two stages ahead, whole 128-byte lines of its rows.
-//   T  comes as codes, 17 bytes a lane and half, three halves ahead; each lane
-//      turns its 32 codes of one row into bf16 and writes them to one of two
+//   T  comes as codes, three halves ahead; each lane turns its 32 or 16 codes of
+//      one row into bf16 and writes them to one of two
 //      LDS tiles, a half ahead of their use.  So every code is converted once a
 //      workgroup, and the turned reads give the operand's eight j of one k.
 // The operands of a step are read while the step before multiplies; the one
 // barrier of a half stands between its two steps, after which the next half's
 // T and the next stage's P are there and the places of the last ones are free.
-template <int BI, int BK, int WI, bool TRANSPOSED>
-__global__ __launch_bounds__(256, BI * BK > 128 * 128 ? 1 : 2) void grad_product_kernel(const GradProductArgs a, int i_tiles,
+template <int BI, int BK, int W, int WI, bool TRANSPOSED>
+__global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradProductArgs a, int i_tiles,
                                                                                      int k_tiles) {
-  constexpr int WK = 4 / WI;
+  constexpr int WK = W / WI;
   constexpr int FI = BI / (32 * WI), FK = BK / (32 * WK);  // 32-wide operands of a wave
   constexpr int P_STAGE = BI * 128, T_HALF = BK * 64;       // bytes
-  constexpr int P_LOADS = P_STAGE / 4096;                   // of 1 KiB, of a wave and stage
-  static_assert(BK == 256 && P_LOADS % 4 == 0, "a thread a chunk of T, a fourth of P's loads a step");
+  constexpr int P_LOADS = P_STAGE / (1024 * W);             // of 1 KiB, of a wave and stage
+  constexpr int PUTS = 16 / W;                              // dwords of codes of a lane and half
+  static_assert(BK == 256 && (W == 4 || W == 8) && P_LOADS % 4 == 0, "all threads share T; a fourth of P's loads a step");
   __shared__ __attribute__((aligned(16))) uint8_t p0[P_STAGE], p1[P_STAGE], p2[P_STAGE], t0[T_HALF], t1[T_HALF];
   const auto p_slot = [&](int s) -> uint8_t * { return s == 0 ? p0 : (s == 1 ? p1 : p2); };
   const auto t_slot = [&](int s) -> uint8_t * { return s == 0 ? t0 : t1; };
@@ -103,96 +110,116 @@ __global__ __launch_bounds__(256, BI * BK > 128 * 128 ? 1 : 2) void grad_product
   const uint16_t *p_base = TRANSPOSED ? a.P + i0 : a.P + (int64_t)i0 * a.ldp;
   constexpr int PC = TRANSPOSED ? BI / 8 : 8;  // chunks of a row in LDS
   constexpr int PR = 64 / PC;                  // rows of a load
-  // The lane's row and chunk of load 0; for transposed rows the chunk of the
-  // loads n and n + 4 is the same.
-  constexpr int PV = TRANSPOSED ? 4 : 1;
+  // The lane's row in load 0, and its chunk, which is the same in loads n and
+  // n + PV.
+  constexpr int PV = TRANSPOSED ? 4 : 2;
   const int pl_row = wave * P_LOADS * PR + lane / PC;
-  int pl_off[PV], pl_j = 0;
+  int pl_off[PV], pl_j[PV];
 #pragma unroll
   for (int v = 0; v < PV; ++v) {
     const int r = pl_row + v * PR;
-    const int c = (lane % PC) ^ (TRANSPOSED ? ((r & 3) << 1) | ((r >> 2) & 1) : r & 7);
+    const int c = (lane % PC) ^ (TRANSPOSED ? turn_swizzle(r) : line_swizzle(r));
     pl_off[v] = pl_row * ld2 + c * 16;
-    pl_j = c * 8;
+    pl_j[v] = c * 8;
   }
-  auto load_p = [&](int stage, int slot, int n) {
-    uint8_t *to = p_slot(slot) + (wave * P_LOADS + n) * 1024;
+  // The buffer of the stage that P's loads are in (of size 0 past the last), and
+  // the lane's offsets; all of it is advanced a stage at a time, since products
+  // of addresses between the matrix instructions take more cycles than those hide.
+  const int j_end = a.J < last * 64 ? a.J : last * 64;
+  const uint16_t *p_at = TRANSPOSED ? p_base + (int64_t)first * 64 * a.ldp : p_base + first * 64;
+  int p_left = j_end - first * 64;  // of j
+  int p_size, p_off[PV];
+  auto enter_p = [&]() {
     if (TRANSPOSED) {
-      const int left = stage < last ? a.J - stage * 64 : 0;
-      const int rows = left < 64 ? left : 64;
-      const __amdgpu_buffer_rsrc_t rs =
-          sized(p_base + (int64_t)(left > 0 ? stage * 64 : 0) * a.ldp, left > 0 ? (rows - 1) * ld2 + rows_i * 2 : 0);
-      load_to_lds(rs, to, pl_off[n % PV], n * PR * ld2);
+      const int rows = p_left < 64 ? p_left : 64;
+      p_size = rows > 0 ? (rows - 1) * ld2 + rows_i * 2 : 0;
     } else {
-      const __amdgpu_buffer_rsrc_t rs = sized(p_base, stage < last ? (rows_i - 1) * ld2 + a.J * 2 : 0);
-      load_to_lds(rs, to, off_or_oob(stage * 64 + pl_j < a.J, pl_off[0]), n * PR * ld2 + stage * 128);
+      p_size = p_left > 0 ? (rows_i - 1) * ld2 + (p_left < 64 ? p_left : 64) * 2 : 0;
     }
+#pragma unroll
+    for (int v = 0; v < PV; ++v) p_off[v] = TRANSPOSED ? pl_off[v] : off_or_oob(pl_j[v] < p_left, pl_off[v]);
+  };
+  auto leave_p = [&]() {
+    p_at += TRANSPOSED ? (int64_t)a.ldp * 64 : 64;
+    p_left -= 64;
+  };
+  auto load_p = [&](int slot, int n) {
+    load_to_lds(sized(p_at, p_size), p_slot(slot) + (wave * P_LOADS + n) * 1024, p_off[n % PV], n * PR * ld2);
   };
 
   // T: row lane % 16 of the half's 16-row group wave % 2, chunk lane / 16 of the
-  // columns' half wave / 2.
+  // columns' half (wave / 2) % 2; of 8 waves each takes 8 of the chunk's 16 bytes.
   struct Raw {
-    u32x4 codes;
+    uint32_t codes[PUTS];
     uint32_t scales;
   } raw[3];
-  const int tg = wave & 1, tc = (lane >> 4) + 4 * (wave >> 1);
+  const int tg = wave & 1, t_high = (wave >> 1) & 1, t_part = (wave >> 2) * PUTS;
+  const int tc = (lane >> 4) + 4 * t_high;
   const int t_row = tg * 16 + (lane & 15);
   const bool t_col = (k0 >> 5) + tc < (a.K >> 5);
-  const int t_code_off = tg * a.K * 8 + ((k0 >> 5) + tc) * 256 + (lane & 15) * 16;
-  auto load_t = [&](int half, int q) {
-    const int j0 = half * 32;
-    const int left = half < 2 * last ? a.J - j0 : 0;
-    const int groups = left <= 0 ? 0 : (left > 16 ? 2 : 1);
-    const int64_t at = left > 0 ? half : 0;
-    const __amdgpu_buffer_rsrc_t rc = sized(a.codes + at * 2 * a.K * 8, groups * a.K * 8);
-    const __amdgpu_buffer_rsrc_t rs = sized(a.scales + at * gp * 32, left > 0 ? gp * 32 : 0);
-    raw[q].codes = __builtin_amdgcn_raw_buffer_load_b128(rc, off_or_oob(t_col, t_code_off), 0, 0);
-    raw[q].scales = __builtin_amdgcn_raw_buffer_load_b32(rs, off_or_oob(t_col && tg < groups, (k0 >> 5) * 32 + lane * 4), 0, 0);
+  const int t_code_off = tg * a.K * 8 + ((k0 >> 5) + tc) * 256 + (lane & 15) * 16 + t_part * 4;
+  const uint8_t *c_at = a.codes + (int64_t)first * 4 * a.K * 8, *s_at = a.scales + (int64_t)first * 2 * gp * 32;
+  int t_left = j_end - first * 64, c_size, s_size;
+  auto enter_t = [&]() {
+    c_size = t_left > 16 ? 2 * a.K * 8 : (t_left > 0 ? a.K * 8 : 0);
+    s_size = t_left > 0 ? gp * 32 : 0;
+  };
+  auto leave_t = [&]() {
+    c_at += 2 * a.K * 8;
+    s_at += gp * 32;
+    t_left -= 32;
+  };
+  const int t_scale_off = off_or_oob(t_col, (k0 >> 5) * 32 + lane * 4), t_code_at = off_or_oob(t_col, t_code_off);
+  auto load_t = [&](int q) {
+    if constexpr (PUTS == 4) {
+      const u32x4 c = __builtin_amdgcn_raw_buffer_load_b128(sized(c_at, c_size), t_code_at, 0, 0);
+      raw[q].codes[0] = c.x, raw[q].codes[1] = c.y, raw[q].codes[2] = c.z, raw[q].codes[3] = c.w;
+    } else {
+      const u32x2 c = __builtin_amdgcn_raw_buffer_load_b64(sized(c_at, c_size), t_code_at, 0, 0);
+      raw[q].codes[0] = c.x, raw[q].codes[1] = c.y;
+    }
+    raw[q].scales = __builtin_amdgcn_raw_buffer_load_b32(sized(s_at, s_size), t_scale_off, 0, 0);
   };
   // Places in LDS, as one address a lane for each pattern of the swizzle; the
   // rest is added as constants.
-  int t_put[4];
+  int t_put[PUTS];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) t_put[c] = turned_at(t_row, 4 * tc + c, BK * 2);
+  for (int c = 0; c < PUTS; ++c) t_put[c] = turned_at(t_row, 4 * tc + t_part + c, BK * 2);
   auto put_t = [&](int q, int slot, int c) {
-    const float scale = __uint_as_float(((raw[q].scales >> (8 * (tg + 2 * (wave >> 1)))) & 0xFF) << 23);
+    const float scale = __uint_as_float(((raw[q].scales >> (8 * (tg + 2 * t_high))) & 0xFF) << 23);
     *(u32x4 *)(t_slot(slot) + t_put[c]) = bf16_of_codes(raw[q].codes[c], scale);
   };
 
   // Operands of a step: columns col + lane % 32, rows 8 * (lane / 32) .. + 7 of
   // the 16 from row j.  The swizzle of a turned read depends on the row modulo 8
-  // (and so on whether it is the first or the second four) and on whether the
-  // column is an even or odd multiple of 32.
+  // (and so on whether it is the first or the second four) and works on the
+  // operand's number modulo 4.
   const int tr_row = (lane >> 5) * 8 + ((lane & 15) >> 2);
   const int tr_col = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-  int t_get[2][2], p_get[4];
+  int t_get[4][2], p_get[4][2];
 #pragma unroll
-  for (int odd = 0; odd < 2; ++odd)
+  for (int n = 0; n < 4; ++n) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int c = (wk + 32 * odd + tr_col) * 2;
-      t_get[odd][q] = turned_at(tr_row + 4 * q, c >> 4, BK * 2) + (c & 15);
-      const int d = (wi + 32 * odd + tr_col) * 2;
-      if (TRANSPOSED) p_get[2 * odd + q] = turned_at(tr_row + 4 * q, d >> 4, BI * 2) + (d & 15);
+      const int c = (wk + 32 * n + tr_col) * 2, d = (wi + 32 * n + tr_col) * 2;
+      t_get[n][q] = turned_at(tr_row + 4 * q, c >> 4, BK * 2) + (c & 15);
+      if (TRANSPOSED) p_get[n][q] = turned_at(tr_row + 4 * q, d >> 4, BI * 2) + (d & 15);
     }
-  if (!TRANSPOSED)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int row = wi + (lane & 31), c = s * 2 + (lane >> 5);
-      p_get[s] = row * 128 + ((c ^ (row & 7)) << 4);
-    }
+    const int row = wi + (lane & 31);
+    if (!TRANSPOSED) p_get[n][0] = row * 128 + (((2 * n + (lane >> 5)) ^ line_swizzle(row)) << 4);
+  }
   bf16x8 tf[2][FK], pf[2][FI];
   // Operand n (of FK + FI) of step `step` (0 .. 3) of the stage in slot p, half in slot t.
   auto read_operand = [&](int to, int step, int p, int t, int n) {
+    static_assert(FK <= 4 && FI <= 4 && FK + FI <= FK * FI, "an address for each operand");
     if (n < FK) {
-      const uint8_t *m = t_slot(t) + (step & 1) * 16 * BK * 2 + (n >> 1) * 128;
-      tf[to][n] = join(read_turned(m + t_get[n & 1][0]), read_turned(m + t_get[n & 1][1]));
+      const uint8_t *m = t_slot(t) + (step & 1) * 16 * BK * 2;
+      tf[to][n] = join(read_turned(m + t_get[n][0]), read_turned(m + t_get[n][1]));
     } else if (TRANSPOSED) {
-      const int y = n - FK;
-      const uint8_t *m = p_slot(p) + step * 16 * BI * 2 + (y >> 1) * 128;
-      pf[to][y] = join(read_turned(m + p_get[2 * (y & 1)]), read_turned(m + p_get[2 * (y & 1) + 1]));
+      const uint8_t *m = p_slot(p) + step * 16 * BI * 2;
+      pf[to][n - FK] = join(read_turned(m + p_get[n - FK][0]), read_turned(m + p_get[n - FK][1]));
     } else {
-      pf[to][n - FK] = *(const bf16x8 *)(p_slot(p) + p_get[step] + (n - FK) * 32 * 128);
+      pf[to][n - FK] = *(const bf16x8 *)(p_slot(p) + p_get[step][0] + (n - FK) * 32 * 128);
     }
   };
 
@@ -207,39 +234,54 @@ __global__ __launch_bounds__(256, BI * BK > 128 * 128 ? 1 : 2) void grad_product
   // One step: its products, and between them the reads of the next step's
   // operands, a fourth of the loads of stage + 2, and in the first step of a half
   // the conversion of the next half and the load of the one after the next two.
-  auto step = [&](int stage, int S, int n_step) {  // S = the stage's slot, all but `stage` known when compiled
+  auto step = [&](int S, int n_step) {  // S: the stage's slot; both known when compiled
     const int h = n_step >> 1, cur = n_step & 1, nxt = cur ^ 1;
     const int half = 2 * S + h;  // modulo 6
     const int next_step = (n_step + 1) & 3, next_p = n_step == 3 ? (S + 1) % 3 : S;
     const int next_t = (n_step & 1) ? (half + 1) & 1 : half & 1;
     constexpr int OPS = FK + FI, MMA = FK * FI;
 #pragma unroll
-    for (int m = 0; m < MMA || m < OPS; ++m) {
+    for (int m = 0; m < MMA; ++m) {
       if (m < OPS) read_operand(nxt, next_step, next_p, next_t, m);
-      if (m < MMA)
-        acc[m / FI][m % FI] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(tf[cur][m / FI], pf[cur][m % FI], acc[m / FI][m % FI], 0, 0, 0);
+      acc[m / FI][m % FI] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(pf[cur][m % FI], tf[cur][m / FI], acc[m / FI][m % FI], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (cur == 0 && m >= 4 && m < 8) put_t((half + 1) % 3, (half + 1) & 1, m - 4);
-      if (cur == 0 && m == 8) load_t(2 * stage + h + 4, (half + 1) % 3);
-      if (m >= 10 && m < 10 + P_LOADS / 4) load_p(stage + 2, (S + 2) % 3, n_step * (P_LOADS / 4) + m - 10);
+      if (cur == 0 && m >= MMA / 4 && m < MMA / 4 + PUTS) put_t((half + 1) % 3, (half + 1) & 1, m - MMA / 4);
+      if (cur == 0 && m == MMA / 2) load_t((half + 1) % 3);
+      if (cur == 0 && m == MMA / 2 + 1) leave_t();
+      if (cur == 1 && m == MMA / 2 + 1) enter_t();
+      if (m >= MMA * 5 / 8 && m < MMA * 5 / 8 + P_LOADS / 4)
+        load_p((S + 2) % 3, n_step * (P_LOADS / 4) + m - MMA * 5 / 8);
+      if (n_step == 3 && m == MMA * 6 / 8) leave_p();
+      if (n_step == 3 && m == MMA * 7 / 8) enter_p();
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  static_assert(FK * FI >= 10 + P_LOADS / 4, "room for the loads between the products");
+  static_assert(FK * FI >= 8 && P_LOADS / 4 <= FK * FI / 8, "room for the loads between the products");
 
   if (first < last) {
     // before the loop: P of two stages, T of the first half, raw T of the next three
+    enter_p();
+    enter_t();
 #pragma unroll
-    for (int n = 0; n < P_LOADS; ++n) load_p(first, 0, n);
-    load_t(2 * first, 0);
-    load_t(2 * first + 1, 1);
-    load_t(2 * first + 2, 2);
+    for (int n = 0; n < P_LOADS; ++n) load_p(0, n);
+    leave_p();
+    enter_p();
 #pragma unroll
-    for (int n = 0; n < P_LOADS; ++n) load_p(first + 1, 1, n);
+    for (int q = 0; q < 3; ++q) {
+      load_t(q);
+      leave_t();
+      enter_t();
+    }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) put_t(0, 0, c);
-    load_t(2 * first + 3, 0);
+    for (int n = 0; n < P_LOADS; ++n) load_p(1, n);
+    leave_p();
+    enter_p();
+#pragma unroll
+    for (int c = 0; c < PUTS; ++c) put_t(0, 0, c);
+    load_t(0);
+    leave_t();
+    enter_t();
     wait_vmcnt<P_LOADS + 6>();  // the first stage's P
     __syncthreads();
 #pragma unroll
@@ -251,7 +293,7 @@ __global__ __launch_bounds__(256, BI * BK > 128 * 128 ? 1 : 2) void grad_product
       for (int S = 0; S < 3; ++S) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          step(stage + S, S, 2 * h);
+          step(S, 2 * h);
           // T of the next half is written and, for the last half, P of the next
           // stage has arrived: 3 / 4 of a stage's loads of P and 4 of T came after
           if (h == 1)
@@ -262,30 +304,73 @@ __global__ __launch_bounds__(256, BI * BK > 128 * 128 ? 1 : 2) void grad_product
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
-          step(stage + S, S, 2 * h + 1);
+          step(S, 2 * h + 1);
         }
       }
     }
-    wait_vmcnt<0>();  // no load may write to LDS that another workgroup has by then
   }
+  wait_vmcnt<0>();  // no load may write to LDS that is used from here on, or by another workgroup
+  __syncthreads();
 
+  // A lane holds column lane % 32 of a 32 x 32 block and rows 8 p + 4 * (lane / 32)
+  // + r.  f32: 32 lanes store 128 bytes of a row.
+  if (a.splits > 1 || a.out_type == 2) {
+    float *const out = a.splits > 1 ? a.partial + (int64_t)blockIdx.y * a.I * a.K : (float *)a.out;
+    const int64_t ld = a.splits > 1 ? a.K : a.ld_out;
 #pragma unroll
-  for (int y = 0; y < FI; ++y) {
-    const int i = i0 + wi + 32 * y + (lane & 31);
-    if (i >= a.I) continue;
-#pragma unroll
-    for (int x = 0; x < FK; ++x)
+    for (int y = 0; y < FI; ++y)
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const int k = k0 + wk + 32 * x + 8 * p + 4 * (lane >> 5);
-        if (k >= a.K) continue;
-        const v4f v = {acc[x][y][4 * p], acc[x][y][4 * p + 1], acc[x][y][4 * p + 2], acc[x][y][4 * p + 3]};
-        if (a.splits > 1)
-          *(v4f *)(a.partial + ((int64_t)blockIdx.y * a.I + i) * a.K + k) = v;
-        else
-          store4(a.out, a.out_type, (int64_t)i * a.ld_out + k, v, a.wide);
+        const int i = i0 + wi + 32 * y + 8 * p + 4 * (lane >> 5);
+        float *const row = out + i * ld + k0 + wk + (lane & 31);
+#pragma unroll
+        for (int x = 0; x < FK; ++x) {
+          if (k0 + wk + 32 * x >= a.K) continue;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (i + r < a.I) row[r * ld + 32 * x] = acc[x][y][4 * p + r];
+        }
       }
+    return;
   }
+  // 16 bits: 32 rows x 64 columns at a time through LDS, so that 8 lanes store 128
+  // bytes of a row.
+  uint16_t *const turn = (uint16_t *)p0 + wave * 32 * 64;
+#pragma unroll
+  for (int y = 0; y < FI; ++y)
+#pragma unroll
+    for (int xx = 0; xx < FK; xx += 2) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 8 * p + 4 * (lane >> 5) + r, col = 32 * x + (lane & 31);
+            const float v = acc[xx + x][y][4 * p + r];
+            turn[row * 64 + (((col >> 3) ^ (row & 7)) << 3) + (col & 7)] =
+                a.out_type == 0 ? __builtin_bit_cast(uint16_t, (__bf16)v) : __builtin_bit_cast(uint16_t, (_Float16)v);
+          }
+      wave_lds_fence();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = 8 * q + (lane >> 3), c = lane & 7;
+        const u32x4 d = *(const u32x4 *)(turn + row * 64 + ((c ^ (row & 7)) << 3));
+        const int i = i0 + wi + 32 * y + row, k = k0 + wk + 32 * xx + 8 * c;
+        if (i >= a.I || k >= a.K) continue;
+        uint16_t *const to = (uint16_t *)a.out + i * a.ld_out + k;
+        if (a.wide) {
+          *(u32x4 *)to = d;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            to[2 * e] = (uint16_t)d[e];
+            to[2 * e + 1] = (uint16_t)(d[e] >> 16);
+          }
+        }
+      }
+      wave_lds_fence();  // before the next columns
+    }
 }
 
 // The splits' sums, in order.
@@ -297,7 +382,7 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const GradProductArgs 
   const int k = (int)(q - i * (a.K >> 2)) * 4;
   v4f v = *(const v4f *)(a.partial + i * a.K + k);
   for (int s = 1; s < a.splits; ++s) v += *(const v4f *)(a.partial + ((int64_t)s * a.I + i) * a.K + k);
-  store4(a.out, a.out_type, i * a.ld_out + k, v, a.wide);
+  store4(a.out, a.out_type, i * a.ld_out + k, v, a.wide4);
 }
 
 // Workgroups that split the sum of one tile: until every CU has one, while
@@ -322,9 +407,9 @@ hipError_t launch_grad_product(GradProductArgs a, hipStream_t stream) {
   const int i_tiles = (a.I + 255) / 256, k_tiles = (a.K + 255) / 256;
   const dim3 grid((unsigned)(i_tiles * k_tiles), a.splits);
   if (a.transposed)
-    grad_product_kernel<256, 256, 2, true><<<grid, 256, 0, stream>>>(a, i_tiles, k_tiles);
+    grad_product_kernel<256, 256, 8, 4, true><<<grid, 512, 0, stream>>>(a, i_tiles, k_tiles);
   else
-    grad_product_kernel<256, 256, 2, false><<<grid, 256, 0, stream>>>(a, i_tiles, k_tiles);
+    grad_product_kernel<256, 256, 8, 2, false><<<grid, 512, 0, stream>>>(a, i_tiles, k_tiles);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits <= 1) return e;
   const int64_t quads = (int64_t)a.I * (a.K / 4);

@@ -152,7 +152,8 @@ mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, const void
   a.J = (int)N;
   a.K = (int)K;
   a.partial = (float *)ws;
-  a.wide = wide4(dx, ld_dx, size_of(dx_type));
+  a.wide = aligned(dx, 16) && ld_dx * size_of(dx_type) % 16 == 0;
+  a.wide4 = wide4(dx, ld_dx, size_of(dx_type));
   return hip_status(launch_grad_product(a, (hipStream_t)stream));
 }
 
@@ -184,7 +185,8 @@ mxfp4_status_t mxfp4_linear_grad_weight(const void *dz, int64_t ld_dz, const voi
   a.I = (int)N;
   a.J = (int)M;
   a.K = (int)K;
-  a.wide = wide4(dw, ld_dw, size_of(dw_type));
+  a.wide = aligned(dw, 16) && ld_dw * size_of(dw_type) % 16 == 0;
+  a.wide4 = wide4(dw, ld_dw, size_of(dw_type));
   if (M > 0) {
     uint8_t *codes = (uint8_t *)ws, *scales = codes + align256(packed_codes_bytes(M, K));
     a.codes = codes;

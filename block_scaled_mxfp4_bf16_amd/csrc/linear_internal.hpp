@@ -73,7 +73,7 @@ struct GradProductArgs {
   int I, J, K;
   float *partial;  // [splits][I][K] in the workspace, if splits > 1
   int splits, split_stages;
-  int wide;
+  int wide, wide4;  // whether out takes 16 bytes, or four elements, in one access
 };
 
 size_t grad_product_workspace_bytes(int64_t I, int64_t J, int64_t K);

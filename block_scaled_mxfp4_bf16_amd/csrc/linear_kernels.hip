@@ -11,9 +11,8 @@ namespace mxfp4 {
 
 // Quantize rows into the prepared layout.  One wave takes one K step of 16
 // rows, as prepare_b does; four lanes share a group of 32 elements.  Rows past
-// the last one and groups past K become zero codes; scale bytes of rows and
-// groups that do not exist are written only where a product reads them with
-// the others of their dword, and meet zero codes.
+// the last one and groups past K become zero codes; where the last 16 rows are
+// the first of their block of 32, the scale bytes of the others are zero too.
 template <bool SW>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint16_t *x, int64_t ld, int rows, int K, uint8_t *codes,
                                                         uint8_t *scales, int steps, int units) {
@@ -39,7 +38,11 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint16_t *x, i
     uint32_t sc;
     const uint32_t d = quant_quarter_t<SW>(w[ch], &sc);
     if (grp < G) to[grp * 64 + lane] = d;
-    if ((lane & 3) == 0 && grp < gp) block[shuffled_scale_offset(row & 31, grp, gp)] = (uint8_t)sc;
+    if ((lane & 3) == 0 && grp < gp) {
+      uint8_t *const at = block + shuffled_scale_offset(row & 31, grp, gp);
+      *at = (uint8_t)sc;
+      if (!(g & 1) && 16 * (g + 1) >= rows) at[1] = 0;  // row + 16
+    }
   }
 }
 
