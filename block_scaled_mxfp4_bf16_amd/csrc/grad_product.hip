@@ -73,8 +73,10 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
   constexpr int FI = BI / (32 * WI), FK = BK / (32 * WK);  // 32-wide operands of a wave
   constexpr int P_STAGE = BI * 128, T_HALF = BK * 64;       // bytes
   constexpr int P_LOADS = P_STAGE / (1024 * W);             // of 1 KiB, of a wave and stage
-  constexpr int PUTS = 16 / W;                              // dwords of codes of a lane and half
-  static_assert(BK == 256 && (W == 4 || W == 8) && P_LOADS % 4 == 0, "all threads share T; a fourth of P's loads a step");
+  constexpr int PUTS = BK / (16 * W);                       // dwords of codes of a lane and half: 8 of each
+  constexpr int SIDES = BK / 128;                           // of 4 chunks of T's rows, a wave's worth of lanes
+  static_assert(SIDES * 128 == BK && (PUTS == 2 || PUTS == 4) && P_LOADS % 4 == 0,
+                "all threads share T; a fourth of P's loads a step");
   __shared__ __attribute__((aligned(16))) uint8_t p0[P_STAGE], p1[P_STAGE], p2[P_STAGE], t0[T_HALF], t1[T_HALF];
   const auto p_slot = [&](int s) -> uint8_t * { return s == 0 ? p0 : (s == 1 ? p1 : p2); };
   const auto t_slot = [&](int s) -> uint8_t * { return s == 0 ? t0 : t1; };
@@ -147,14 +149,16 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
     load_to_lds(sized(p_at, p_size), p_slot(slot) + (wave * P_LOADS + n) * 1024, p_off[n % PV], n * PR * ld2);
   };
 
-  // T: row lane % 16 of the half's 16-row group wave % 2, chunk lane / 16 of the
-  // columns' half (wave / 2) % 2; of 8 waves each takes 8 of the chunk's 16 bytes.
+  // T: row lane % 16 of the half's 16-row group wave % 2, chunk lane / 16 of side
+  // (wave / 2) % SIDES of the columns; where that leaves waves over, each takes 8
+  // of the chunk's 16 bytes.
   struct Raw {
     uint32_t codes[PUTS];
     uint32_t scales;
   } raw[3];
-  const int tg = wave & 1, t_high = (wave >> 1) & 1, t_part = (wave >> 2) * PUTS;
-  const int tc = (lane >> 4) + 4 * t_high;
+  const int tg = wave & 1, side = (wave >> 1) % SIDES, t_part = (wave / (2 * SIDES)) * PUTS;
+  const int tc = (lane >> 4) + 4 * side;
+  const int t_high = ((k0 >> 7) + side) & 1;  // the scales of 8 groups lie together, 4 by 4
   const int t_row = tg * 16 + (lane & 15);
   const bool t_col = (k0 >> 5) + tc < (a.K >> 5);
   const int t_code_off = tg * a.K * 8 + ((k0 >> 5) + tc) * 256 + (lane & 15) * 16 + t_part * 4;
@@ -169,7 +173,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
     s_at += gp * 32;
     t_left -= 32;
   };
-  const int t_scale_off = off_or_oob(t_col, (k0 >> 5) * 32 + lane * 4), t_code_at = off_or_oob(t_col, t_code_off);
+  const int t_scale_off = off_or_oob(t_col, (k0 >> 8) * 256 + lane * 4), t_code_at = off_or_oob(t_col, t_code_off);
   auto load_t = [&](int q) {
     if constexpr (PUTS == 4) {
       const u32x4 c = __builtin_amdgcn_raw_buffer_load_b128(sized(c_at, c_size), t_code_at, 0, 0);
@@ -231,6 +235,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.f;
 
+  constexpr int MMA_SLOTS = FK * FI - FK * FI * 5 / 8;
   // One step: its products, and between them the reads of the next step's
   // operands, a fourth of the loads of stage + 2, and in the first step of a half
   // the conversion of the next half and the load of the one after the next two.
@@ -257,7 +262,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  static_assert(FK * FI >= 8 && P_LOADS / 4 <= FK * FI / 8, "room for the loads between the products");
+  static_assert(FK * FI >= 4 && MMA_SLOTS >= P_LOADS / 4, "room for the loads between the products");
 
   if (first < last) {
     // before the loop: P of two stages, T of the first half, raw T of the next three
@@ -373,6 +378,132 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
     }
 }
 
+// Few rows of P (32 * FI at most): reading T bounds it, and nothing waits at a
+// barrier before the sums.  64 columns a workgroup; its waves and the splits
+// take every 32 of j in turn, D of them loaded ahead.  A lane turns one chunk of
+// 32 codes into bf16 in its wave's own 4 KiB of LDS, P's rows go straight to
+// registers.  The waves' sums meet in LDS, in wave order.
+constexpr int kFewWaves = 8;
+template <int FI, int D>
+__global__ __launch_bounds__(64 * kFewWaves) void grad_few_kernel(const GradProductArgs a) {
+  constexpr int W = kFewWaves;
+  __shared__ __attribute__((aligned(16))) float red[W][2][16][64];  // and before that the waves' tiles of T
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k0 = blockIdx.x * 64;
+  const int G = a.K >> 5, gp = (G + 7) & ~7;
+  const int units = (a.J + 31) >> 5;
+  uint8_t *const tile = (uint8_t *)red + wave * 4096;
+
+  // T: row lane % 16 of group lane / 32, chunk (lane / 16) % 2
+  const int tg = lane >> 5, tc = (k0 >> 5) + ((lane >> 4) & 1), tr = lane & 15;
+  const bool t_col = tc < G;
+  const int t_bytes = ((a.J + 15) >> 4) * a.K * 8, s_bytes = ((a.J + 31) >> 5) * gp * 32;
+  const __amdgpu_buffer_rsrc_t c_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)a.codes, 0, t_bytes, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)a.scales, 0, s_bytes, kRsrcWord3);
+  const int c_off = off_or_oob(t_col, tg * a.K * 8 + tc * 256 + tr * 16);
+  const int s_off = off_or_oob(t_col, (tc >> 3) * 256 + (tr << 2) + ((tc & 3) << 6));
+  const int s_shift = 8 * (tg + 2 * ((tc >> 2) & 1));
+  const int ld2 = (int)a.ldp * 2;
+  const __amdgpu_buffer_rsrc_t p_rsrc =
+      __builtin_amdgcn_make_buffer_rsrc((void *)a.P, 0, (a.I - 1) * ld2 + a.J * 2, kRsrcWord3);
+  const int p_j = 8 * (lane >> 5);
+  int p_off[FI];
+#pragma unroll
+  for (int y = 0; y < FI; ++y) {
+    const int i = 32 * y + (lane & 31);
+    p_off[y] = off_or_oob(i < a.I, i * ld2 + p_j * 2);
+  }
+
+  struct Stage {
+    u32x4 codes;
+    uint32_t scale;
+    u32x4 p[2][FI];
+  } st[D];
+  auto load = [&](int q, int u) {
+    st[q].codes = __builtin_amdgcn_raw_buffer_load_b128(c_rsrc, off_or_oob(u < units, c_off), u * 2 * a.K * 8, 0);
+    st[q].scale = __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, off_or_oob(u < units && 32 * u + 16 * tg < a.J, s_off),
+                                                       u * gp * 32, 0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int y = 0; y < FI; ++y)
+        st[q].p[s][y] = __builtin_amdgcn_raw_buffer_load_b128(
+            p_rsrc, off_or_oob(32 * u + 16 * s + p_j < a.J, p_off[y]), u * 64 + s * 32, 0);
+  };
+  const auto place = [](int j, int c) { return j * 128 + ((c ^ (((j & 2) << 1) | ((j >> 2) & 1))) << 4); };
+  const int tr_row = (lane >> 5) * 8 + ((lane & 15) >> 2);
+  const int tr_col = (((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
+
+  v16f acc[2][FI];
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int y = 0; y < FI; ++y)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.f;
+  auto compute = [&](int q) {
+    const float scale = __uint_as_float(((st[q].scale >> s_shift) & 0xFF) << 23);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *(u32x4 *)(tile + place(tg * 16 + tr, 4 * ((lane >> 4) & 1) + c)) = bf16_of_codes(st[q].codes[c], scale);
+    wave_lds_fence();
+    bf16x8 t[2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = 16 * s + tr_row, c = 64 * x + tr_col;
+        t[s][x] = join(read_turned(tile + place(j, c >> 4) + (c & 15)), read_turned(tile + place(j + 4, c >> 4) + (c & 15)));
+      }
+    wave_lds_fence();  // before the next unit's codes
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < FI; ++y)
+          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, st[q].p[s][y]), t[s][x], acc[x][y],
+                                                              0, 0, 0);
+  };
+
+  const int stride = W * gridDim.y, first = blockIdx.y * W + wave;
+#pragma unroll
+  for (int q = 0; q < D; ++q) load(q, first + q * stride);
+  for (int u = first; u < units; u += D * stride)
+#pragma unroll
+    for (int q = 0; q < D; ++q) {  // units past the last are zeros
+      compute(q);
+      load(q, u + (D + q) * stride);
+    }
+
+  const bool split = gridDim.y > 1;
+#pragma unroll
+  for (int y = 0; y < FI; ++y) {
+    if (32 * y >= a.I) break;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) red[wave][x][r][lane] = acc[x][y][r];
+    __syncthreads();
+    const int row = threadIdx.x >> 4, c = (threadIdx.x & 15) * 4;
+    const int i = 32 * y + row, k = k0 + c;
+    if (i < a.I && k < a.K) {
+      const auto part = [&](int w) {
+        return *(const v4f *)&red[w][c >> 5][4 * (row >> 3) + (row & 3)][((row >> 2) & 1) * 32 + (c & 31)];
+      };
+      v4f v = part(0);
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += part(w);
+      if (split)
+        *(v4f *)(a.partial + ((int64_t)blockIdx.y * a.I + i) * a.K + k) = v;
+      else
+        store4(a.out, a.out_type, (int64_t)i * a.ld_out + k, v, a.wide4);
+    }
+  }
+}
+
 // The splits' sums, in order.
 __global__ __launch_bounds__(256) void join_splits_kernel(const GradProductArgs a) {
   const int64_t quads = (int64_t)a.I * (a.K >> 2);
@@ -385,32 +516,81 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const GradProductArgs 
   store4(a.out, a.out_type, i * a.ld_out + k, v, a.wide4);
 }
 
-// Workgroups that split the sum of one tile: until every CU has one, while
-// each keeps 256 of j.
-static int64_t splits_of(int64_t I, int64_t J, int64_t K) {
-  const int64_t tiles = ((I + 255) / 256) * ((K + 255) / 256), most = J / 256;
-  const int64_t want = 256 / tiles;
-  const int64_t s = want < most ? want : most;
-  return s < 1 ? 1 : s;
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a product is done: the form, and over how many workgroups the sum of one
+// tile is split.
+struct Plan {
+  enum { kFew, kTile128, kTile256 } form;
+  int splits, split_stages;
+};
+
+// Splits of `units` of j for `tiles` tiles: until every CU has a workgroup, and
+// no fewer than `least` units each.
+int64_t split_count(int64_t tiles, int64_t units, int64_t least) {
+  const int64_t want = cdiv(256, tiles), most = units / least;
+  return want < most ? (want < 1 ? 1 : want) : (most < 1 ? 1 : most);
 }
 
-size_t grad_product_workspace_bytes(int64_t I, int64_t J, int64_t K) {
-  const int64_t s = splits_of(I, J, K);
-  return s > 1 ? (size_t)s * (size_t)I * (size_t)K * 4 : 0;
+Plan plan_of(int64_t I, int64_t J, int64_t K, bool transposed) {
+  Plan p{Plan::kTile256, 1, 0};
+  if (!transposed && I <= 128) {
+    p.form = Plan::kFew;
+    p.splits = (int)split_count(cdiv(K, 64), cdiv(J, 32), kFewWaves * 2);
+    return p;
+  }
+  const int64_t stages = cdiv(J, 64);
+  int64_t tiles = cdiv(I, 256) * cdiv(K, 256);
+  if (tiles < 192) {
+    p.form = Plan::kTile128;
+    tiles = cdiv(I, 128) * cdiv(K, 128);
+  }
+  // rounds of three stages
+  const int64_t want = tiles < 192 ? split_count(tiles, stages, 3) : 1;
+  p.split_stages = (int)(cdiv(cdiv(stages, want), 3) * 3);
+  p.splits = stages > 0 ? (int)cdiv(stages, p.split_stages) : 1;
+  return p;
+}
+
+template <int BI, int BK, int W, int WI, bool TRANSPOSED>
+void run_tiles(const GradProductArgs &a, hipStream_t stream) {
+  const int i_tiles = (int)cdiv(a.I, BI), k_tiles = (int)cdiv(a.K, BK);
+  const dim3 grid((unsigned)(i_tiles * k_tiles), a.splits);
+  grad_product_kernel<BI, BK, W, WI, TRANSPOSED><<<grid, 64 * W, 0, stream>>>(a, i_tiles, k_tiles);
+}
+
+}  // namespace
+
+size_t grad_product_workspace_bytes(int64_t I, int64_t J, int64_t K, bool transposed) {
+  const Plan p = plan_of(I, J, K, transposed);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)I * (size_t)K * 4 : 0;
 }
 
 hipError_t launch_grad_product(GradProductArgs a, hipStream_t stream) {
-  const int stages = (a.J + 63) / 64;
-  const int64_t want = splits_of(a.I, a.J, a.K);
-  a.split_stages = (int)((stages + want - 1) / want);
-  a.splits = a.split_stages > 0 ? (stages + a.split_stages - 1) / a.split_stages : 1;
-  const int i_tiles = (a.I + 255) / 256, k_tiles = (a.K + 255) / 256;
-  const dim3 grid((unsigned)(i_tiles * k_tiles), a.splits);
-  if (a.transposed)
-    grad_product_kernel<256, 256, 8, 4, true><<<grid, 512, 0, stream>>>(a, i_tiles, k_tiles);
-  else
-    grad_product_kernel<256, 256, 8, 2, false><<<grid, 512, 0, stream>>>(a, i_tiles, k_tiles);
-  hipError_t e = hipGetLastError();
+  const Plan p = plan_of(a.I, a.J, a.K, a.transposed);
+  a.splits = p.splits;
+  a.split_stages = p.split_stages;
+  if (p.form == Plan::kFew) {
+    const dim3 grid((unsigned)cdiv(a.K, 64), a.splits);
+    if (a.I <= 32)
+      grad_few_kernel<1, 4><<<grid, 64 * kFewWaves, 0, stream>>>(a);
+    else if (a.I <= 64)
+      grad_few_kernel<2, 3><<<grid, 64 * kFewWaves, 0, stream>>>(a);
+    else
+      grad_few_kernel<4, 2><<<grid, 64 * kFewWaves, 0, stream>>>(a);
+  } else if (p.form == Plan::kTile128) {
+    if (a.transposed)
+      run_tiles<128, 128, 4, 2, true>(a, stream);
+    else
+      run_tiles<128, 128, 4, 2, false>(a, stream);
+  } else if (a.transposed) {
+    run_tiles<256, 256, 8, 4, true>(a, stream);
+  } else {
+    run_tiles<256, 256, 8, 2, false>(a, stream);
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits <= 1) return e;
   const int64_t quads = (int64_t)a.I * (a.K / 4);
   join_splits_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(a);

@@ -121,7 +121,7 @@ mxfp4_status_t mxfp4_linear_grad_pre(const void *dy, int dy_type, int64_t ld_dy,
 }
 
 size_t mxfp4_linear_grad_input_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M < 1 || N < 1 || K < 1 || !sizes_fit(M, N, K) ? 0 : grad_product_workspace_bytes(M, N, K);
+  return M < 1 || N < 1 || K < 1 || !sizes_fit(M, N, K) ? 0 : grad_product_workspace_bytes(M, N, K, false);
 }
 
 mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, const void *Bq_sh, const void *Bs_sh, void *dx,
@@ -137,7 +137,7 @@ mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, const void
   if (M == 0) return MXFP4_OK;
   HeldWorkspace held;
   void *ws = nullptr;
-  const mxfp4_status_t st = take_workspace(workspace, workspace_bytes, grad_product_workspace_bytes(M, N, K),
+  const mxfp4_status_t st = take_workspace(workspace, workspace_bytes, grad_product_workspace_bytes(M, N, K, false),
                                            (hipStream_t)stream, &held, &ws);
   if (st != MXFP4_OK) return st;
   GradProductArgs a{};
@@ -160,7 +160,7 @@ mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, const void
 size_t mxfp4_linear_grad_weight_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return M < 1 || N < 1 || K < 1 || !sizes_fit(M, N, K)
              ? 0
-             : align256(packed_bytes(M, K)) + grad_product_workspace_bytes(N, M, K);
+             : align256(packed_bytes(M, K)) + grad_product_workspace_bytes(N, M, K, true);
 }
 
 mxfp4_status_t mxfp4_linear_grad_weight(const void *dz, int64_t ld_dz, const void *x, int64_t ldx, void *dw,
@@ -172,7 +172,7 @@ mxfp4_status_t mxfp4_linear_grad_weight(const void *dz, int64_t ld_dz, const voi
   if (!vector_rows(dz, ld_dz) || !vector_rows(x, ldx) || !aligned(dw, size_of(dw_type))) return MXFP4_ERR_INVALID_ARG;
   HeldWorkspace held;
   void *ws = nullptr;
-  const size_t need = M > 0 ? align256(packed_bytes(M, K)) + grad_product_workspace_bytes(N, M, K) : 0;
+  const size_t need = M > 0 ? align256(packed_bytes(M, K)) + grad_product_workspace_bytes(N, M, K, true) : 0;
   const mxfp4_status_t st = take_workspace(workspace, workspace_bytes, need, (hipStream_t)stream, &held, &ws);
   if (st != MXFP4_OK) return st;
   GradProductArgs a{};

@@ -76,7 +76,7 @@ struct GradProductArgs {
   int wide, wide4;  // whether out takes 16 bytes, or four elements, in one access
 };
 
-size_t grad_product_workspace_bytes(int64_t I, int64_t J, int64_t K);
+size_t grad_product_workspace_bytes(int64_t I, int64_t J, int64_t K, bool transposed);
 hipError_t launch_grad_product(GradProductArgs a, hipStream_t stream);
 
 // Quantize `rows` rows of bf16, ld elements apart, into the prepared layout.
