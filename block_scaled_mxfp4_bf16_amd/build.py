@@ -17,7 +17,7 @@ PROBES_SOURCES = ["probes.hip", "probe_phases.hip", "probe_wide.hip"]
 PROBES_LIB = os.path.join(PKG, "libmxfp4_probes.so")
 SOURCES = ["mxfp4_api.hip", "quant_kernels.hip", "gemm_kernels.hip", "gemm_wide.hip", "experts_api.hip",
            "gemv_kernels.hip", "route_kernels.hip", "combine_kernels.hip",
-           "grouped_kernels.hip", "linear_api.hip", "linear_kernels.hip", "grad_kernels.hip", "grad_product.hip"] + [
+           "grouped_kernels.hip", "linear_api.hip", "linear_kernels.hip", "linear_tile.hip", "grad_kernels.hip", "grad_product.hip"] + [
     "gemm_table_%d.hip" % i for i in range(8)]
 ARCH = "gfx950"
 
@@ -41,7 +41,7 @@ HIPCC_FLAGS = [
 # instructions; keeping accumulators in VGPRs lets them update in place.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA_FLAGS = {"gemm_wide.hip": VGPR_FORM, "gemv_kernels.hip": VGPR_FORM, "grouped_kernels.hip": VGPR_FORM,
-               "linear_kernels.hip": VGPR_FORM, "probes.hip": VGPR_FORM, "probe_wide.hip": VGPR_FORM}
+               "linear_kernels.hip": VGPR_FORM, "linear_tile.hip": VGPR_FORM, "probes.hip": VGPR_FORM, "probe_wide.hip": VGPR_FORM}
 
 
 def hipcc() -> str:

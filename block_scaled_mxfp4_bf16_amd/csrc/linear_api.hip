@@ -20,6 +20,9 @@ inline bool sizes_fit(int64_t M, int64_t N, int64_t K) {
 // Whether vectors of four elements of `size` bytes at p, rows ld apart, are aligned.
 inline bool wide4(const void *p, int64_t ld, int64_t size) { return !p || (aligned(p, 4 * size) && ld % 4 == 0); }
 
+// ... and pieces of 16 bytes.
+inline bool lines(const void *p, int64_t ld, int64_t size) { return !p || (aligned(p, 16) && ld * size % 16 == 0); }
+
 // A matrix that the kernels read in 16-byte pieces of bf16.
 inline bool vector_rows(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
@@ -77,6 +80,9 @@ mxfp4_status_t mxfp4_linear(const void *x, int64_t ldx, const void *Bq_sh, const
   a.ws = (uint8_t *)ws;
   a.wide_y = wide4(y, ldy, size_of(y_type)) && wide4(residual, ld_res, size_of(y_type));
   a.wide_pre = wide4(pre, ld_pre, 2);
+  a.wide_bias = !bias || aligned(bias, 4 * size_of(bias_type));
+  a.line_y = lines(y, ldy, size_of(y_type)) && lines(residual, ld_res, size_of(y_type));
+  a.line_pre = lines(pre, ld_pre, 2);
   return hip_status(launch_linear(a, (hipStream_t)stream));
 }
 
@@ -152,7 +158,7 @@ mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, const void
   a.J = (int)N;
   a.K = (int)K;
   a.partial = (float *)ws;
-  a.wide = aligned(dx, 16) && ld_dx * size_of(dx_type) % 16 == 0;
+  a.wide = lines(dx, ld_dx, size_of(dx_type));
   a.wide4 = wide4(dx, ld_dx, size_of(dx_type));
   return hip_status(launch_grad_product(a, (hipStream_t)stream));
 }
@@ -185,7 +191,7 @@ mxfp4_status_t mxfp4_linear_grad_weight(const void *dz, int64_t ld_dz, const voi
   a.I = (int)N;
   a.J = (int)M;
   a.K = (int)K;
-  a.wide = aligned(dw, 16) && ld_dw * size_of(dw_type) % 16 == 0;
+  a.wide = lines(dw, ld_dw, size_of(dw_type));
   a.wide4 = wide4(dw, ld_dw, size_of(dw_type));
   if (M > 0) {
     uint8_t *codes = (uint8_t *)ws, *scales = codes + align256(packed_codes_bytes(M, K));

@@ -131,4 +131,109 @@ __device__ __forceinline__ void store4(void *p, int type, int64_t i, const v4f &
   }
 }
 
+// Barrier of LDS written by the memory system: the caller has waited for its
+// own loads; nothing may move across.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// activate() of eight values, the choice outside.
+__device__ __forceinline__ void activate8(int act, float (&z)[8]) {
+  switch (act) {
+    case kActNone: break;
+#define MXFP4_EACH(KIND)                                     \
+  case KIND:                                                 \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) z[i] = activate(KIND, z[i]); \
+    break;
+      MXFP4_EACH(kActRelu)
+      MXFP4_EACH(kActSilu)
+      MXFP4_EACH(kActGelu)
+      MXFP4_EACH(kActGeluTanh)
+#undef MXFP4_EACH
+  }
+}
+
+// Eight neighbouring elements of a runtime type.
+__device__ __forceinline__ void load8(const void *p, int type, int64_t i, int wide, float (&v)[8]) {
+  const v4f a = load4(p, type, i, wide), b = load4(p, type, i + 4, wide);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+}
+
+__device__ __forceinline__ void unpack8(const u32x4 &d, int type, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w = d[j];
+    if (type == 0) {
+      v[2 * j] = __uint_as_float(w << 16);
+      v[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+      const f16x2 h = __builtin_bit_cast(f16x2, w);
+      v[2 * j] = (float)h.x;
+      v[2 * j + 1] = (float)h.y;
+    }
+  }
+}
+
+// ... at a byte offset of a buffer, where an offset out of range reads zeros and
+// stores nothing.  `wide`: 16 bytes at a time.
+__device__ __forceinline__ void load8_buffer(const __amdgpu_buffer_rsrc_t &r, int type, int off, int wide, float (&v)[8]) {
+  if (type == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      u32x4 d;
+      if (wide) {
+        d = __builtin_amdgcn_raw_buffer_load_b128(r, off, 4 * j, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 4 * (j + i), 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j + i] = __uint_as_float(d[i]);
+    }
+    return;
+  }
+  u32x4 d;
+  if (wide) {
+    d = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      d[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 4 * i, 0) |
+             (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 4 * i + 2, 0) << 16;
+  }
+  unpack8(d, type, v);
+}
+__device__ __forceinline__ void store8(const __amdgpu_buffer_rsrc_t &r, int type, int off, const float (&v)[8], int wide) {
+  if (type == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      u32x4 d;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(v[j + i]);
+      if (wide) {
+        __builtin_amdgcn_raw_buffer_store_b128(d, r, off, 4 * j, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b32(d[i], r, off, 4 * (j + i), 0);
+      }
+    }
+    return;
+  }
+  u32x4 d;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d[j] = type == 0 ? bf16x2_rne(v[2 * j], v[2 * j + 1]) : f16x2_rne(v[2 * j], v[2 * j + 1]);
+  if (wide) {
+    __builtin_amdgcn_raw_buffer_store_b128(d, r, off, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)d[i], r, off, 4 * i, 0);
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(d[i] >> 16), r, off, 4 * i + 2, 0);
+    }
+  }
+}
+
 }  // namespace mxfp4

@@ -36,11 +36,13 @@ struct LinearArgs {
   uint8_t *ws;
   // set by launch_linear
   uint8_t *codes, *scales;  // of the quantized rows, in ws
-  int wide_y, wide_pre;     // whether four columns go in one access
+  int wide_y, wide_pre, wide_bias;  // whether four columns go in one access (y's also of the residual)
+  int line_y, line_pre;             // ... or 16 bytes
 };
 
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear(LinearArgs a, hipStream_t stream);
+hipError_t launch_linear_tile(const LinearArgs &a, hipStream_t stream);  // rows quantized
 
 struct GradPreArgs {
   const void *dy;

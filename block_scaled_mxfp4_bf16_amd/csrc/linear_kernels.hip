@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const uint16_t *x, i
 
 hipError_t launch_pack_rows(const uint16_t *x, int64_t ld, int64_t rows, int64_t K, uint8_t *codes, uint8_t *scales,
                             bool sw, hipStream_t stream) {
-  const int steps = (int)((K + 127) / 128);
+  const int steps = (int)((K / 32 + 7) / 8 * 2);  // the scales' padding included
   const int64_t units = (rows + 15) / 16 * steps;
   const unsigned blocks = (unsigned)((units + 3) / 4);
   if (sw)
@@ -158,6 +158,13 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
   }
 }
 
+// Whether 256 x 256 tiles are the faster form: one for most CUs.  Gated ones need
+// their pairs of column groups whole.
+static bool use_tiles(const LinearArgs &a) {
+  const int64_t m_tiles = (a.M + 255) / 256, n_tiles = ((int64_t)a.N + 255) / 256;
+  return m_tiles * n_tiles >= 128 && (!a.gated || a.N % 64 == 0);
+}
+
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return packed_bytes(M, K); }
 
 hipError_t launch_linear(LinearArgs a, hipStream_t stream) {
@@ -165,6 +172,7 @@ hipError_t launch_linear(LinearArgs a, hipStream_t stream) {
   a.scales = a.ws + (packed_codes_bytes(a.M, a.K) + 255) / 256 * 256;
   const hipError_t e = launch_pack_rows(a.x, a.ldx, a.M, a.K, a.codes, a.scales, a.sw, stream);
   if (e != hipSuccess) return e;
+  if (use_tiles(a)) return launch_linear_tile(a, stream);
   const int cols = a.gated ? a.N / 2 : a.N, width = a.gated ? 32 : 64;
   const int n_tiles = (cols + width - 1) / width;
   const int m_tiles = (a.M + 63) / 64;
