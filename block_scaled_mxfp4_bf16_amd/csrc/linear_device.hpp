@@ -177,6 +177,11 @@ __device__ __forceinline__ void unpack8(const u32x4 &d, int type, float (&v)[8])
   }
 }
 
+// Cache policy of a store: past the caches.  What a large product writes would
+// displace what it reads from L2 otherwise (8192 x 16384 x 2048, bf16: 232 us
+// through the caches, 193 past them).
+constexpr int kPastCaches = 2;
+
 // ... at a byte offset of a buffer, where an offset out of range reads zeros and
 // stores nothing.  `wide`: 16 bytes at a time.
 __device__ __forceinline__ void load8_buffer(const __amdgpu_buffer_rsrc_t &r, int type, int off, int wide, float (&v)[8]) {
@@ -214,7 +219,7 @@ __device__ __forceinline__ void store8(const __amdgpu_buffer_rsrc_t &r, int type
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(v[j + i]);
       if (wide) {
-        __builtin_amdgcn_raw_buffer_store_b128(d, r, off, 4 * j, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(d, r, off, 4 * j, kPastCaches);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b32(d[i], r, off, 4 * (j + i), 0);
@@ -226,7 +231,7 @@ __device__ __forceinline__ void store8(const __amdgpu_buffer_rsrc_t &r, int type
 #pragma unroll
   for (int j = 0; j < 4; ++j) d[j] = type == 0 ? bf16x2_rne(v[2 * j], v[2 * j + 1]) : f16x2_rne(v[2 * j], v[2 * j + 1]);
   if (wide) {
-    __builtin_amdgcn_raw_buffer_store_b128(d, r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(d, r, off, 0, kPastCaches);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

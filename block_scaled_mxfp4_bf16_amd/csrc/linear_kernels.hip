@@ -59,12 +59,15 @@ hipError_t launch_pack_rows(const uint16_t *x, int64_t ld, int64_t rows, int64_t
 }
 
 // 16 * MW rows x 16 * NT weight rows a workgroup; the WK waves take every
-// WK-th K step, hold the whole tile's sums and add them through LDS in wave
-// order.  Nothing waits at a barrier before that.  The weights are the first
-// operand of the instruction, so a lane holds four neighbouring columns of a
-// row.  Gated: the first NT / 2 weight groups are gate columns, the others
-// their up columns.
-template <int MW, int NT, int WK>
+// WK-th K step, D of them loaded ahead, hold the whole tile's sums and add them
+// through LDS in wave order.  Nothing waits at a barrier before that.  The weights
+// are the first operand of the instruction, so a lane holds four neighbouring
+// columns of a row.  Gated: the first NT / 2 weight groups are gate columns, the
+// others their up columns.
+// PACKED: the rows come quantized.  Otherwise each wave quantizes them on its
+// way: the operand's lane has 32 elements of one row, a whole group, so the
+// scale is found and the codes are made without another lane's help.
+template <int MW, int NT, int WK, int D, bool PACKED>
 __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs a, int n_tiles) {
   __shared__ __attribute__((aligned(16))) v4f red[WK][MW * NT][64];
   const int lane = threadIdx.x & 63;
@@ -81,18 +84,24 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
   const int64_t b_bytes = (int64_t)groups * K * 8, s_bytes = (int64_t)((N + 255) >> 8) * 8 * gp * 32;
   const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)a.Bw, 0, (int)b_bytes, kRsrcWord3);
   const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)a.Bs, 0, (int)s_bytes, kRsrcWord3);
+  // the rows: their codes and scales, or themselves
   const int own_groups = x_groups - xg0 < MW ? x_groups - xg0 : MW;
-  const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(a.codes + (int64_t)xg0 * K * 8), 0, own_groups * K * 8, kRsrcWord3);
+  const int ldx = (int)a.ldx * 2;
+  const int own_rows = a.M - row0 < 16 * MW ? a.M - row0 : 16 * MW;
+  const __amdgpu_buffer_rsrc_t x_rsrc =
+      PACKED ? __builtin_amdgcn_make_buffer_rsrc((void *)(a.codes + (int64_t)xg0 * K * 8), 0, own_groups * K * 8, kRsrcWord3)
+             : __builtin_amdgcn_make_buffer_rsrc((void *)(a.x + (int64_t)row0 * a.ldx), 0, (own_rows - 1) * ldx + K * 2,
+                                                 kRsrcWord3);
   const __amdgpu_buffer_rsrc_t xs_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(a.scales + (int64_t)(xg0 >> 1) * gp * 32), 0, (((xg0 & 1) + own_groups + 1) >> 1) * gp * 32, kRsrcWord3);
+      (void *)(a.scales + (int64_t)(xg0 >> 1) * gp * 32), 0,
+      PACKED ? (((xg0 & 1) + own_groups + 1) >> 1) * gp * 32 : 0, kRsrcWord3);
 
   int gw[NT];
   bool gok[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (a.gated) {
-      const int c = n_tile * (NT / 2) + nt % (NT / 2);
+      const int c = n_tile * (NT / 2) + nt % (NT > 1 ? NT / 2 : 1);
       gok[nt] = c < (groups >> 1);
       gw[nt] = nt < NT / 2 ? c : (groups >> 1) + c;
     } else {
@@ -106,32 +115,69 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  for (int ks = wave; ks < KS; ks += WK) {
+  struct Stage {
+    u32x4 x[MW][PACKED ? 1 : 4], b[NT];
+    uint32_t xs[MW], bs[NT];
+  } st[D];
+  auto load = [&](int q, int ks) __attribute__((always_inline)) {
     // a K chunk past the end meets zeros of the rows; it must not run past
     // the matrix all the same
     const bool ok = (4 * ks + q4) * 32 < K;
-    u32x4 x[MW], b[NT];
-    uint32_t xs[MW], bs[NT];
+    if (!PACKED)
+#pragma unroll
+      for (int mt = 0; mt < MW; ++mt) {
+        const int row = 16 * mt + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st[q].x[mt][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              x_rsrc, off_or_oob(ok && row < own_rows, row * ldx + ks * 256 + q4 * 64 + 16 * i), 0, 0);
+      }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
+      st[q].b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
           b_rsrc, off_or_oob(ok && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
-      bs[nt] = __builtin_amdgcn_raw_buffer_load_b32(
-          s_rsrc, off_or_oob(gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
+      st[q].bs[nt] = __builtin_amdgcn_raw_buffer_load_b32(
+          s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
     }
+    if (PACKED)
+#pragma unroll
+      for (int mt = 0; mt < MW; ++mt) {
+        st[q].x[mt][0] =
+            __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, off_or_oob(ok, mt * K * 8 + ks * 1024 + lane * 16), 0, 0);
+        st[q].xs[mt] = __builtin_amdgcn_raw_buffer_load_b32(
+            xs_rsrc, off_or_oob(ok, (((xg0 & 1) + mt) >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
+      }
+  };
+  auto compute = [&](int q, int ks) __attribute__((always_inline)) {
+    u32x4 x[MW];
+    uint32_t xs[MW];
 #pragma unroll
     for (int mt = 0; mt < MW; ++mt) {
-      x[mt] = __builtin_amdgcn_raw_buffer_load_b128(x_rsrc, off_or_oob(ok, mt * K * 8 + ks * 1024 + lane * 16), 0, 0);
-      xs[mt] = __builtin_amdgcn_raw_buffer_load_b32(
-          xs_rsrc, (((xg0 & 1) + mt) >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4, 0, 0);
+      if (PACKED) {
+        x[mt] = st[q].x[mt][0];
+        xs[mt] = st[q].xs[mt] >> (8 * (((xg0 + mt) & 1) + 2 * (ks & 1)));
+      } else {
+        uint32_t w[16], c[4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = st[q].x[mt][PACKED ? 0 : i >> 2][i & 3];
+        xs[mt] = a.sw ? quant_group32<true>(w, c) : quant_group32<false>(w, c);
+        x[mt] = u32x4{c[0], c[1], c[2], c[3]};
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < MW; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        acc[mt][nt] = mfma_fp4(b[nt], x[mt], acc[mt][nt], bs[nt] >> (8 * ((gw[nt] & 1) + 2 * (ks & 1))),
-                               xs[mt] >> (8 * (((xg0 + mt) & 1) + 2 * (ks & 1))));
-  }
+        acc[mt][nt] = mfma_fp4(st[q].b[nt], x[mt], acc[mt][nt], st[q].bs[nt] >> (8 * ((gw[nt] & 1) + 2 * (ks & 1))), xs[mt]);
+  };
+#pragma unroll
+  for (int q = 0; q < D; ++q) load(q, wave + q * WK);
+  for (int ks = wave; ks < KS; ks += D * WK)
+#pragma unroll
+    for (int q = 0; q < D; ++q) {  // steps past the last are zeros
+      compute(q, ks + q * WK);
+      load(q, ks + (D + q) * WK);
+    }
 #pragma unroll
   for (int mt = 0; mt < MW; ++mt)
 #pragma unroll
@@ -165,18 +211,32 @@ static bool use_tiles(const LinearArgs &a) {
   return m_tiles * n_tiles >= 128 && (!a.gated || a.N % 64 == 0);
 }
 
-size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return packed_bytes(M, K); }
+// Rows that are quantized on the way, in one launch.
+constexpr int kFewRows = 16;
+
+size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewRows ? 0 : packed_bytes(M, K); }
+
+template <int MW, int NT, int WK, int D, bool PACKED>
+static void run_split(const LinearArgs &a, hipStream_t stream) {
+  const int cols = a.gated ? a.N / 2 : a.N, width = a.gated ? 8 * NT : 16 * NT;
+  const int n_tiles = (cols + width - 1) / width, m_tiles = (a.M + 16 * MW - 1) / (16 * MW);
+  linear_split_kernel<MW, NT, WK, D, PACKED><<<(unsigned)((int64_t)n_tiles * m_tiles), 64 * WK, 0, stream>>>(a, n_tiles);
+}
 
 hipError_t launch_linear(LinearArgs a, hipStream_t stream) {
+  if (a.M <= kFewRows) {
+    if (a.gated)
+      run_split<1, 2, 8, 2, false>(a, stream);
+    else
+      run_split<1, 1, 8, 2, false>(a, stream);
+    return hipGetLastError();
+  }
   a.codes = a.ws;
   a.scales = a.ws + (packed_codes_bytes(a.M, a.K) + 255) / 256 * 256;
   const hipError_t e = launch_pack_rows(a.x, a.ldx, a.M, a.K, a.codes, a.scales, a.sw, stream);
   if (e != hipSuccess) return e;
   if (use_tiles(a)) return launch_linear_tile(a, stream);
-  const int cols = a.gated ? a.N / 2 : a.N, width = a.gated ? 32 : 64;
-  const int n_tiles = (cols + width - 1) / width;
-  const int m_tiles = (a.M + 63) / 64;
-  linear_split_kernel<4, 4, 4><<<(unsigned)((int64_t)n_tiles * m_tiles), 256, 0, stream>>>(a, n_tiles);
+  run_split<4, 4, 4, 3, true>(a, stream);
   return hipGetLastError();
 }
 

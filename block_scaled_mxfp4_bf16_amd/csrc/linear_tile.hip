@@ -11,8 +11,10 @@
 // barrier a step, between its halves.
 // Workgroups stay and walk over tiles; the loads run on into the next tile while
 // the last steps and the epilogue of this one are under way.
-// The sums leave through LDS, 8 rows x 64 columns a wave at a time, so that a lane
-// has 8 neighbouring columns of a row and 8 lanes a row's whole 128-byte line.
+// The sums of two neighbouring blocks change places between lanes, after which a
+// lane has 8 neighbouring columns of a row and four lanes 64 bytes of bf16.  (Turned
+// in LDS, 8 rows x 64 columns a wave at a time, a tile's epilogue took 13 us for
+// the 8 us of this form, most of it waiting for LDS.)
 #include "linear_epilogue.hpp"
 #include "linear_internal.hpp"
 
@@ -58,9 +60,9 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   constexpr int FI = 4, FK = 8;               // 16-row blocks of a wave: rows, weight rows
   constexpr int BN = GATED ? 128 : 256;       // output columns of a tile
   constexpr int kStores = GATED ? 8 : 16;     // of y, at least, by a wave and tile
+  constexpr int kPreStores = 16;  // of the kept z
   __shared__ __attribute__((aligned(16))) uint8_t s0[kSlot], s1[kSlot], s2[kSlot], s3[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t c0[kScales], c1[kScales];
-  __shared__ __attribute__((aligned(16))) uint8_t turned[8 * 2048];
   const auto slot = [&](int s) -> uint8_t * { return s == 0 ? s0 : (s == 1 ? s1 : (s == 2 ? s2 : s3)); };
   const auto scale_slot = [&](int s) -> uint8_t * { return s == 0 ? c0 : c1; };
 
@@ -88,8 +90,8 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
     int x_size, xs_size, w_size, ws_size;
     int b_off[2], s_off;  // of the weight blocks that this wave loads
   };
-  bool none = false;  // no tile was left for the last find()
-  auto find = [&]() {
+  int none = 0;  // whether no tile was left for the last find()
+  auto find = [&]() __attribute__((always_inline)) {
     Tile u;
     none = next >= end;
     const int t = none ? 0 : next;
@@ -116,6 +118,10 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
     }
     const int g = GATED ? ((wave >> 1) & 1) * (N >> 6) + (u.n0 >> 5) + (wave >> 2) * 2 + (wave & 1) : (u.n0 >> 5) + wave;
     u.s_off = g * gp * 32;
+    // The quotients come from the vector unit, and the compiler may leave all that
+    // follows from them there, the loads' buffers among it.
+    asm("" : "+s"(u.m0), "+s"(u.n0), "+s"(u.x), "+s"(u.xs), "+s"(u.b_off[0]), "+s"(u.b_off[1]), "+s"(u.s_off));
+    asm("" : "+s"(u.x_size), "+s"(u.xs_size), "+s"(u.w_size), "+s"(u.ws_size));
     return u;
   };
   Tile cur = find();           // of the loads
@@ -125,25 +131,25 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   const int l16 = lane * 16, l4 = lane * 4, l_k = (lane >> 4) * 32;
   // Loads of step lk into a slot: this wave's two blocks of rows, its two of
   // weights, and of even steps its two blocks of scales.
-  auto load_rows = [&](int to) {
+  auto load_rows = [&](int to) __attribute__((always_inline)) {
     const int off = off_or_oob(lk * 128 + l_k < K, l16);  // chunks past K are zeros here, whatever the weights' are
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       block_to_lds(sized(cur.x, cur.x_size), slot(to) + (2 * wave + q) * 1024, off, (2 * wave + q) * K * 8 + lk * 1024);
   };
-  auto load_weights = [&](int to) {
+  auto load_weights = [&](int to) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       block_to_lds(sized(a.Bw, cur.w_size), slot(to) + (16 + 2 * wave + q) * 1024, l16, cur.b_off[q] + lk * 1024);
   };
-  auto load_scales = [&](int to) {
+  auto load_scales = [&](int to) __attribute__((always_inline)) {
     const bool ok = (lk >> 1) * 8 < gp;
     scales_to_lds(sized(cur.xs, ok ? cur.xs_size : 0), scale_slot(to) + wave * 256, l4, wave * gp * 32 + (lk >> 1) * 256);
     scales_to_lds(sized(a.Bs, ok ? cur.ws_size : 0), scale_slot(to) + 2048 + wave * 256, l4, cur.s_off + (lk >> 1) * 256);
   };
   // On to the next step, or the next tile; selects, since a branch would let the
   // compiler move the products into one of its ways.
-  auto leave = [&](bool last) {
+  auto leave = [&](bool last) __attribute__((always_inline)) {
     lk = last ? 0 : lk + 1;
     cur.x = last ? after.x : cur.x;
     cur.xs = last ? after.xs : cur.xs;
@@ -160,10 +166,10 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   // a prepared scale dword: byte g + 2 o is that of group g of its 32 rows in step
   // o of its two.
   u32x4 xf[FI], wf[FK];
-  auto read_weights = [&](int s, int x) { wf[x] = *(const u32x4 *)(slot(s) + (16 + 8 * wk + x) * 1024 + l16); };
-  auto read_rows = [&](int s, int y) { xf[y] = *(const u32x4 *)(slot(s) + (4 * wi + y) * 1024 + l16); };
+  auto read_weights = [&](int s, int x) __attribute__((always_inline)) { wf[x] = *(const u32x4 *)(slot(s) + (16 + 8 * wk + x) * 1024 + l16); };
+  auto read_rows = [&](int s, int y) __attribute__((always_inline)) { xf[y] = *(const u32x4 *)(slot(s) + (4 * wi + y) * 1024 + l16); };
   uint32_t xs[2][FI / 2], ws[2][FK / 2];
-  auto read_scales = [&](int s) {
+  auto read_scales = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < FK / 2; ++n) ws[s][n] = *(const uint32_t *)(scale_slot(s) + 2048 + (4 * wk + n) * 256 + l4);
 #pragma unroll
@@ -171,7 +177,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   };
 
   v4f acc[FK][FI];
-  auto clear = [&]() {
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int x = 0; x < FK; ++x)
 #pragma unroll
@@ -183,7 +189,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   // each block of weights is followed by the next step's in the same registers.
   // Between the products the loads go out: the barrier has freed slot s, which
   // takes the step four on, its rows at once and its weights in the next half.
-  auto half_step = [&](int s, int h, bool last) __attribute__((always_inline)) {
+  auto half_step = [&](int s, int h, int past) __attribute__((always_inline)) {
     const int sp = s >> 1, next = (s + 1) & 3;
 #pragma unroll
     for (int x = 0; x < FK; ++x) {
@@ -196,7 +202,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
       if (h == 0) {
         if (x < 2) read_rows(s, 2 + x);
         if (x == 3) load_weights((s + 3) & 3);
-        if (x == 5) leave(s == 0 && last);
+        if (x == 5) leave(s == 0 && past >= 0);
       } else {
         read_weights(next, x);
         if (x < 2) read_rows(next, x);
@@ -208,23 +214,18 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
     }
   };
 
-  // Eight neighbouring columns of a row, f32, through LDS: 8 rows x 64 columns of
-  // the wave at a time, chunk c (4 columns) of row r at 256 r + 16 (c ^ 2 r).
-  uint8_t *const turn = turned + wave * 2048;
-  auto to_rows = [&](int x, int y, int q, int lane, float (&v)[8]) __attribute__((always_inline)) {  // blocks x .. x + 3, rows 8 q .. 8 q + 7 of row block y
-    if (((lane & 15) >> 3) == q) {
-      const int r = lane & 7;
+  // A lane holds columns 4 g .. 4 g + 3, g = lane / 16, of a block's row lane % 16.
+  // Swapping lanes 16 - 31 of one block's sums with lanes 0 - 15 of the next one's
+  // (and 48 - 63 with 32 - 47) leaves it eight neighbouring columns: pieces 0, 2, 1
+  // and 3 of the two blocks' 32 for g = 0 .. 3.
+  auto neighbours = [&](int x, int y, float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *(v4f *)(turn + r * 256 + (((4 * b + (lane >> 4)) ^ (2 * r)) << 4)) = acc[x + b][y];
+    for (int i = 0; i < 4; ++i) {
+      uint32_t p = __float_as_uint(acc[x][y][i]), q = __float_as_uint(acc[x + 1][y][i]);
+      swap16(p, q);
+      v[i] = __uint_as_float(p);
+      v[4 + i] = __uint_as_float(q);
     }
-    wave_lds_fence();
-    const int r = lane >> 3, c = 2 * (lane & 7);
-    const v4f lo = *(const v4f *)(turn + r * 256 + ((c ^ (2 * r)) << 4));
-    const v4f hi = *(const v4f *)(turn + r * 256 + (((c + 1) ^ (2 * r)) << 4));
-    wave_lds_fence();  // before the next rows
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
   };
   auto epilogue = [&](int row0, int col0) __attribute__((always_inline)) {
     // The lane's number is found anew for each tile, from a zero that the compiler
@@ -243,9 +244,10 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
         sized((const uint8_t *)a.residual + (int64_t)row0 * ldr, a.residual ? (rows - 1) * ldr + cols * size : 0);
     const __amdgpu_buffer_rsrc_t p_rsrc =
         sized((uint8_t *)a.pre + (int64_t)row0 * ldp, a.pre ? (rows - 1) * ldp + N * 2 : 0);
+    const int piece = ((lane >> 5) & 1) | ((lane >> 3) & 2);
 #pragma unroll
-    for (int pair = 0; pair < (GATED ? 1 : 2); ++pair) {
-      const int col = col0 + (GATED ? 64 : 128) * wk + 64 * pair + 8 * (lane & 7);
+    for (int pair = 0; pair < (GATED ? 2 : 4); ++pair) {
+      const int col = col0 + (GATED ? 64 : 128) * wk + 32 * pair + 8 * piece;
       const bool col_ok = col < cols;
       float bias[8], bias_up[8];
       if (a.bias) {
@@ -260,61 +262,43 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
         }
       }
 #pragma unroll
-      for (int y = 0; y < FI; ++y)
+      for (int y = 0; y < FI; ++y) {
+        const int row = 64 * wi + 16 * y + (lane & 15);
+        const bool ok = col_ok && row < rows;
+        float z[8], up[8];
+        neighbours(2 * pair, y, z);
+        if (GATED) neighbours(4 + 2 * pair, y, up);
+        if (a.bias) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int row = 64 * wi + 16 * y + 8 * q + (lane >> 3);
-          const bool ok = col_ok && row < rows;
-          float z[8], up[8];
-          to_rows(4 * pair, y, q, lane, z);
-          if (GATED) to_rows(4, y, q, lane, up);
-          if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              z[i] += bias[i];
-              if (GATED) up[i] += bias_up[i];
-            }
+          for (int i = 0; i < 8; ++i) {
+            z[i] += bias[i];
+            if (GATED) up[i] += bias_up[i];
           }
-          if (a.pre) {
-            store8(p_rsrc, 0, off_or_oob(ok, row * ldp + col * 2), z, a.line_pre);
-            if (GATED) store8(p_rsrc, 0, off_or_oob(ok, row * ldp + (half + col) * 2), up, a.line_pre);
-          }
-          activate8(a.act, z);
-          if (GATED) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] *= up[i];
-          }
-          if (a.residual) {
-            float r[8];
-            load8_buffer(r_rsrc, a.y_type, off_or_oob(ok, row * ldr + col * size), a.line_y, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] += r[i];
-          }
-          store8(y_rsrc, a.y_type, off_or_oob(ok, row * ldy + col * size), z, a.line_y);
-          __builtin_amdgcn_sched_barrier(0);  // few values at a time: the sums fill the registers
         }
+        if (a.pre) {
+          store8(p_rsrc, 0, off_or_oob(ok, row * ldp + col * 2), z, a.line_pre);
+          if (GATED) store8(p_rsrc, 0, off_or_oob(ok, row * ldp + (half + col) * 2), up, a.line_pre);
+        }
+        activate8(a.act, z);
+        if (GATED) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] *= up[i];
+        }
+        if (a.residual) {
+          float r[8];
+          load8_buffer(r_rsrc, a.y_type, off_or_oob(ok, row * ldr + col * size), a.line_y, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] += r[i];
+        }
+        store8(y_rsrc, a.y_type, off_or_oob(ok, row * ldy + col * size), z, a.line_y);
+        __builtin_amdgcn_sched_barrier(0);  // few values at a time: the sums fill the registers
+      }
     }
   };
 
-  // Four steps.  fresh (known when compiled): the first after another tile's
-  // stores, which may still be under way then.  last: the tile's last ones.
-  auto round = [&](bool fresh, bool last) __attribute__((always_inline)) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      half_step(s, 0, last);
-      // the next step's blocks, and its scales, have arrived for every wave, and
-      // every wave has read this step's; 10 loads came after them
-      if (fresh && s < 2)
-        wait_vmcnt<10 + kStores>();
-      else
-        wait_vmcnt<10>();
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      __builtin_amdgcn_sched_barrier(0);
-      lds_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      half_step(s, 1, last);
-    }
-    // the sums stay where they are: the compiler must not put products off
+  // The sums stay where they are: the compiler must not put products off past a
+  // branch.
+  auto hold = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int x = 0; x < FK; ++x)
 #pragma unroll
@@ -338,22 +322,43 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   read_rows(0, 1);
   read_scales(0);
   clear();
-  int ks = 0;
+  int fresh = 0;  // the first steps after another tile's stores, which may still be under way; 2: with z among them
   for (;;) {
-    for (; ks < steps; ks += 4) round(false, ks + 4 >= steps);
+    for (int ks = 0; ks < steps; ks += 4) {
+      const int past = __builtin_amdgcn_readfirstlane(ks + 4 - steps);  // the tile's end
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        half_step(s, 0, past);
+        // the next step's blocks, and its scales, have arrived for every wave, and
+        // every wave has read this step's; 10 loads came after them
+        if (s < 2) {
+          hold();
+          if (fresh == 2)
+            wait_vmcnt<10 + kStores + kPreStores>();
+          else if (fresh)
+            wait_vmcnt<10 + kStores>();
+          else
+            wait_vmcnt<10>();
+        } else {
+          wait_vmcnt<10>();
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        half_step(s, 1, past);
+      }
+      hold();
+      fresh = 0;
+    }
     const bool more = !none;
     epilogue(row0, col0);
     if (!more) break;
     row0 = after.m0, col0 = after.n0;
     after = find();
     clear();
-    if (!a.line_y || (a.pre && !a.line_pre)) {
-      wait_vmcnt<0>();  // more stores than are counted
-      ks = 0;
-    } else {
-      round(true, 4 >= steps);
-      ks = 4;
-    }
+    fresh = a.line_y && (!a.pre || a.line_pre) ? (a.pre ? 2 : 1) : 0;
+    if (!fresh) wait_vmcnt<0>();  // more stores than are counted
   }
   wait_vmcnt<0>();  // no load may write to LDS that another workgroup has by then
 }
