@@ -547,10 +547,25 @@ Plan plan_of(int64_t I, int64_t J, int64_t K, bool transposed) {
     p.form = Plan::kTile128;
     tiles = cdiv(I, 128) * cdiv(K, 128);
   }
-  // rounds of three stages
-  const int64_t want = tiles < 192 ? split_count(tiles, stages, 3) : 1;
-  p.split_stages = (int)(cdiv(cdiv(stages, want), 3) * 3);
-  p.splits = stages > 0 ? (int)cdiv(stages, p.split_stages) : 1;
+  p.split_stages = (int)(cdiv(stages, 3) * 3);  // rounds of three stages
+  if (p.form != Plan::kTile128) return p;
+  // 128 x 128 tiles take 0.62 us a stage while two workgroups fit on every CU.  A
+  // split costs its launch and what crosses the chiplets' caches, 5 us, and the
+  // partial sums' way to memory and back, at 4 MB a us.  (Whole and in three:
+  // 771 rows of 2112 x 704, 13 stages, 16.1 and 22.0 us a call; 3136 rows, 49
+  // stages, 38.8 and 30.0.  256 rows of 4096 x 4096, 64 stages: 40.7 whole, 22.3 in
+  // four.)
+  double best = 0;
+  for (int s = 1; s <= 16 && 3 * (s - 1) < stages; ++s) {
+    const int64_t per = cdiv(cdiv(stages, s), 3) * 3;
+    const double rounds = tiles * s > 512 ? tiles * s / 512.0 : 1.0;
+    const double t = 0.62 * per * rounds + (s > 1 ? 5 + s * (double)I * K * 8 / 4e6 : 0);
+    if (s > 1 && t >= best) continue;
+    best = t;
+    p.split_stages = (int)per;
+    p.splits = (int)cdiv(stages, per);
+  }
+  if (p.splits < 1) p.splits = 1;
   return p;
 }
 
