@@ -470,12 +470,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void grad_few_kernel(const GradProd
   const int stride = W * gridDim.y, first = blockIdx.y * W + wave;
 #pragma unroll
   for (int q = 0; q < D; ++q) load(q, first + q * stride);
-  for (int u = first; u < units; u += D * stride)
+  // units past the last are zeros; the last round loads nothing
+  int u = first;
+  for (; u - wave + D * stride < units; u += D * stride)
 #pragma unroll
-    for (int q = 0; q < D; ++q) {  // units past the last are zeros
+    for (int q = 0; q < D; ++q) {
       compute(q);
       load(q, u + (D + q) * stride);
     }
+#pragma unroll
+  for (int q = 0; q < D; ++q) compute(q);
 
   const bool split = gridDim.y > 1;
 #pragma unroll

@@ -184,32 +184,35 @@ constexpr int kPastCaches = 2;
 
 // ... at a byte offset of a buffer, where an offset out of range reads zeros and
 // stores nothing.  `wide`: 16 bytes at a time.
-__device__ __forceinline__ void load8_buffer(const __amdgpu_buffer_rsrc_t &r, int type, int off, int wide, float (&v)[8]) {
-  if (type == 2) {
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      u32x4 d;
-      if (wide) {
-        d = __builtin_amdgcn_raw_buffer_load_b128(r, off, 4 * j, 0);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 4 * (j + i), 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[j + i] = __uint_as_float(d[i]);
-    }
-    return;
-  }
-  u32x4 d;
+struct Raw8 {
+  u32x4 d[2];  // the second of f32 only
+};
+__device__ __forceinline__ Raw8 load_raw8(const __amdgpu_buffer_rsrc_t &r, int type, int off, int wide) {
+  Raw8 v;
   if (wide) {
-    d = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    v.d[0] = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    if (type == 2) v.d[1] = __builtin_amdgcn_raw_buffer_load_b128(r, off, 16, 0);
+  } else if (type == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.d[i >> 2][i & 3] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 4 * i, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      d[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 4 * i, 0) |
-             (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 4 * i + 2, 0) << 16;
+      v.d[0][i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 4 * i, 0) |
+                  (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 4 * i + 2, 0) << 16;
   }
-  unpack8(d, type, v);
+  return v;
+}
+__device__ __forceinline__ void add_raw8(const Raw8 &r, int type, float (&v)[8]) {
+  if (type == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(r.d[i >> 2][i & 3]);
+  } else {
+    float f[8];
+    unpack8(r.d[0], type, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += f[i];
+  }
 }
 __device__ __forceinline__ void store8(const __amdgpu_buffer_rsrc_t &r, int type, int off, const float (&v)[8], int wide) {
   if (type == 2) {

@@ -172,12 +172,16 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
   };
 #pragma unroll
   for (int q = 0; q < D; ++q) load(q, wave + q * WK);
-  for (int ks = wave; ks < KS; ks += D * WK)
+  // steps past the last are zeros; the last round loads nothing
+  int ks = wave;
+  for (; ks - wave + D * WK < KS; ks += D * WK)
 #pragma unroll
-    for (int q = 0; q < D; ++q) {  // steps past the last are zeros
+    for (int q = 0; q < D; ++q) {
       compute(q, ks + q * WK);
       load(q, ks + (D + q) * WK);
     }
+#pragma unroll
+  for (int q = 0; q < D; ++q) compute(q, ks + q * WK);
 #pragma unroll
   for (int mt = 0; mt < MW; ++mt)
 #pragma unroll
@@ -211,10 +215,15 @@ static bool use_tiles(const LinearArgs &a) {
   return m_tiles * n_tiles >= 128 && (!a.gated || a.N % 64 == 0);
 }
 
-// Rows that are quantized on the way, in one launch.
-constexpr int kFewRows = 16;
+// Whether the rows are quantized on the way, in one launch: 16 of them at most,
+// and as every workgroup reads all of them, 192 KiB.  us so and with a launch of
+// their own, captured: 13 rows of 4096 x 4096 6.3 and 6.4; 2112 x 7168, 2 rows 6.3
+// and 7.5, 8 rows 7.8 and 7.6, 13 rows 8.9 and 7.4; 13 rows of 4096 x 1024 4.6 and
+// 5.8.  A call that is not captured pays 2 us more for the second launch: the 13
+// rows of 2112 x 7168 take 9.6 and 10.6.
+static bool in_one_launch(int64_t M, int64_t K) { return M <= 16 && M * K <= 98304; }
 
-size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return M <= kFewRows ? 0 : packed_bytes(M, K); }
+size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return in_one_launch(M, K) ? 0 : packed_bytes(M, K); }
 
 template <int MW, int NT, int WK, int D, bool PACKED>
 static void run_split(const LinearArgs &a, hipStream_t stream) {
@@ -224,11 +233,16 @@ static void run_split(const LinearArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_linear(LinearArgs a, hipStream_t stream) {
-  if (a.M <= kFewRows) {
-    if (a.gated)
+  if (in_one_launch(a.M, a.K)) {
+    // 16, 32 or 64 weight rows a workgroup, so that there are 256 of them at most,
+    // about.  us for one row: 4096 x 4096 4.6, 6.0 (16 and 32); gated 16384 x 4096 8.6
+    // and 6.9 (32 and 64).
+    if (!a.gated && a.N <= 4096)
+      run_split<1, 1, 8, 2, false>(a, stream);
+    else if (a.N <= 8192)
       run_split<1, 2, 8, 2, false>(a, stream);
     else
-      run_split<1, 1, 8, 2, false>(a, stream);
+      run_split<1, 4, 8, 2, false>(a, stream);
     return hipGetLastError();
   }
   a.codes = a.ws;
@@ -236,7 +250,19 @@ hipError_t launch_linear(LinearArgs a, hipStream_t stream) {
   const hipError_t e = launch_pack_rows(a.x, a.ldx, a.M, a.K, a.codes, a.scales, a.sw, stream);
   if (e != hipSuccess) return e;
   if (use_tiles(a)) return launch_linear_tile(a, stream);
-  run_split<4, 4, 4, 3, true>(a, stream);
+  // Small tiles make more workgroups, large ones read less: the smallest of which
+  // every CU has one at most, about.  us a call with 32 x 32, 32 x 64 and 32 x 128
+  // weight rows a workgroup: 32 rows of 4096 x 4096 7.0, 8.0 and 11.5; 128 rows 9.6,
+  // 8.6 and 12.0; 512 rows 22.3, 19.4 and 17.5.
+  const int64_t m_tiles = (a.M + 31) / 32;
+  if (a.M <= 16)
+    run_split<1, 2, 8, 2, true>(a, stream);
+  else if (m_tiles * ((a.N + 31) / 32) <= 256)
+    run_split<2, 2, 8, 2, true>(a, stream);
+  else if (m_tiles * ((a.N + 63) / 64) <= 288)
+    run_split<2, 4, 8, 2, true>(a, stream);
+  else
+    run_split<2, 8, 4, 2, true>(a, stream);
   return hipGetLastError();
 }
 

@@ -245,52 +245,63 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
     const __amdgpu_buffer_rsrc_t p_rsrc =
         sized((uint8_t *)a.pre + (int64_t)row0 * ldp, a.pre ? (rows - 1) * ldp + N * 2 : 0);
     const int piece = ((lane >> 5) & 1) | ((lane >> 3) & 2);
+    constexpr int PAIRS = GATED ? 2 : 4;
+    const auto column = [&](int pair) { return col0 + (GATED ? 64 : 128) * wk + 32 * pair + 8 * piece; };
+    float bias[PAIRS][GATED ? 2 : 1][8];
+    if (a.bias) {
 #pragma unroll
-    for (int pair = 0; pair < (GATED ? 2 : 4); ++pair) {
-      const int col = col0 + (GATED ? 64 : 128) * wk + 32 * pair + 8 * piece;
-      const bool col_ok = col < cols;
-      float bias[8], bias_up[8];
-      if (a.bias) {
-        load8(a.bias, a.bias_type, col_ok ? col : 0, a.wide_bias, bias);
-        if (GATED) load8(a.bias, a.bias_type, half + (col_ok ? col : 0), a.wide_bias, bias_up);
-        // waited for here: a load that seems to be under way when the next tile
-        // begins would make its products wait for all others
+      for (int pair = 0; pair < PAIRS; ++pair) {
+        const int col = column(pair) < cols ? column(pair) : 0;
+        load8(a.bias, a.bias_type, col, a.wide_bias, bias[pair][0]);
+        if (GATED) load8(a.bias, a.bias_type, half + col, a.wide_bias, bias[pair][GATED ? 1 : 0]);
+      }
+      // waited for here: a load that seems to be under way when the next tile
+      // begins would make its products wait for all others
+#pragma unroll
+      for (int pair = 0; pair < PAIRS; ++pair)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          asm volatile("" : "+v"(bias[i]));
-          if (GATED) asm volatile("" : "+v"(bias_up[i]));
+          asm volatile("" : "+v"(bias[pair][0][i]));
+          if (GATED) asm volatile("" : "+v"(bias[pair][GATED ? 1 : 0][i]));
         }
+    }
+#pragma unroll
+    for (int pair = 0; pair < PAIRS; ++pair) {
+      const int col = column(pair);
+      const bool col_ok = col < cols;
+      const auto offset = [&](int y, int ld, int col_bytes) {
+        const int row = 64 * wi + 16 * y + (lane & 15);
+        return off_or_oob(col_ok && row < rows, row * ld + col_bytes);
+      };
+      // the residual of all four row blocks before the first is used
+      Raw8 r[FI];
+      if (a.residual) {
+#pragma unroll
+        for (int y = 0; y < FI; ++y) r[y] = load_raw8(r_rsrc, a.y_type, offset(y, ldr, col * size), a.line_y);
       }
 #pragma unroll
       for (int y = 0; y < FI; ++y) {
-        const int row = 64 * wi + 16 * y + (lane & 15);
-        const bool ok = col_ok && row < rows;
         float z[8], up[8];
         neighbours(2 * pair, y, z);
         if (GATED) neighbours(4 + 2 * pair, y, up);
         if (a.bias) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            z[i] += bias[i];
-            if (GATED) up[i] += bias_up[i];
+            z[i] += bias[pair][0][i];
+            if (GATED) up[i] += bias[pair][GATED ? 1 : 0][i];
           }
         }
         if (a.pre) {
-          store8(p_rsrc, 0, off_or_oob(ok, row * ldp + col * 2), z, a.line_pre);
-          if (GATED) store8(p_rsrc, 0, off_or_oob(ok, row * ldp + (half + col) * 2), up, a.line_pre);
+          store8(p_rsrc, 0, offset(y, ldp, col * 2), z, a.line_pre);
+          if (GATED) store8(p_rsrc, 0, offset(y, ldp, (half + col) * 2), up, a.line_pre);
         }
         activate8(a.act, z);
         if (GATED) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[i] *= up[i];
         }
-        if (a.residual) {
-          float r[8];
-          load8_buffer(r_rsrc, a.y_type, off_or_oob(ok, row * ldr + col * size), a.line_y, r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] += r[i];
-        }
-        store8(y_rsrc, a.y_type, off_or_oob(ok, row * ldy + col * size), z, a.line_y);
+        if (a.residual) add_raw8(r[y], a.y_type, z);
+        store8(y_rsrc, a.y_type, offset(y, ldy, col * size), z, a.line_y);
         __builtin_amdgcn_sched_barrier(0);  // few values at a time: the sums fill the registers
       }
     }
@@ -316,12 +327,15 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   }
   wait_vmcnt<12>();  // after step 0: blocks of steps 1 to 3, 4 + 4 + 2, and scales, 2
   lds_barrier();
+  const auto begin = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int x = 0; x < FK; ++x) read_weights(0, x);
-  read_rows(0, 0);
-  read_rows(0, 1);
-  read_scales(0);
-  clear();
+    for (int x = 0; x < FK; ++x) read_weights(0, x);
+    read_rows(0, 0);
+    read_rows(0, 1);
+    read_scales(0);
+    clear();
+  };
+  begin();
   int fresh = 0;  // the first steps after another tile's stores, which may still be under way; 2: with z among them
   for (;;) {
     for (int ks = 0; ks < steps; ks += 4) {
@@ -356,7 +370,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
     if (!more) break;
     row0 = after.m0, col0 = after.n0;
     after = find();
-    clear();
+    begin();  // the last step has read the operands too, but the epilogue needs their registers
     fresh = a.line_y && (!a.pre || a.line_pre) ? (a.pre ? 2 : 1) : 0;
     if (!fresh) wait_vmcnt<0>();  // more stores than are counted
   }
