@@ -420,16 +420,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void grad_few_kernel(const GradProd
     uint32_t scale;
     u32x4 p[2][FI];
   } st[D];
-  auto load = [&](int q, int u) {
-    st[q].codes = __builtin_amdgcn_raw_buffer_load_b128(c_rsrc, off_or_oob(u < units, c_off), u * 2 * a.K * 8, 0);
-    st[q].scale = __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, off_or_oob(u < units && 32 * u + 16 * tg < a.J, s_off),
-                                                       u * gp * 32, 0);
+  auto load = [&](int q, int unit) {
+    // past the last unit the lanes' offsets alone say so: with a uniform part of
+    // 2^31 the sum of the two would be small again
+    const bool ok = unit < units;
+    const int u = ok ? unit : 0;
+    st[q].codes = __builtin_amdgcn_raw_buffer_load_b128(c_rsrc, off_or_oob(ok, c_off), u * 2 * a.K * 8, 0);
+    st[q].scale =
+        __builtin_amdgcn_raw_buffer_load_b32(s_rsrc, off_or_oob(ok && 32 * u + 16 * tg < a.J, s_off), u * gp * 32, 0);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int y = 0; y < FI; ++y)
         st[q].p[s][y] = __builtin_amdgcn_raw_buffer_load_b128(
-            p_rsrc, off_or_oob(32 * u + 16 * s + p_j < a.J, p_off[y]), u * 64 + s * 32, 0);
+            p_rsrc, off_or_oob(ok && 32 * u + 16 * s + p_j < a.J, p_off[y]), u * 64 + s * 32, 0);
   };
   const auto place = [](int j, int c) { return j * 128 + ((c ^ (((j & 2) << 1) | ((j >> 2) & 1))) << 4); };
   const int tr_row = (lane >> 5) * 8 + ((lane & 15) >> 2);

@@ -68,11 +68,12 @@ hipError_t launch_pack_rows(const uint16_t *x, int64_t ld, int64_t rows, int64_t
 // way: the operand's lane has 32 elements of one row, a whole group, so the
 // scale is found and the codes are made without another lane's help.
 template <int MW, int NT, int WK, int D, bool PACKED>
-__global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs a, int n_tiles) {
+__global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs a, int n_tiles, int first_m) {
   __shared__ __attribute__((aligned(16))) v4f red[WK][MW * NT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m_tile = blockIdx.x / n_tiles, n_tile = blockIdx.x - m_tile * n_tiles;
+  const int m_here = blockIdx.x / n_tiles, n_tile = blockIdx.x - m_here * n_tiles;
+  const int m_tile = first_m + m_here;
   const int K = a.K, N = a.N;
   const int KS = (K + 127) >> 7;
   const int gp = ((K >> 5) + 7) & ~7;
@@ -228,8 +229,14 @@ size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return in_one_l
 template <int MW, int NT, int WK, int D, bool PACKED>
 static void run_split(const LinearArgs &a, hipStream_t stream) {
   const int cols = a.gated ? a.N / 2 : a.N, width = a.gated ? 8 * NT : 16 * NT;
-  const int n_tiles = (cols + width - 1) / width, m_tiles = (a.M + 16 * MW - 1) / (16 * MW);
-  linear_split_kernel<MW, NT, WK, D, PACKED><<<(unsigned)((int64_t)n_tiles * m_tiles), 64 * WK, 0, stream>>>(a, n_tiles);
+  const int64_t n_tiles = (cols + width - 1) / width;
+  const int m_tiles = (a.M + 16 * MW - 1) / (16 * MW);
+  // a grid dimension holds fewer than 2^32 threads
+  const int most = (int)(((int64_t)1 << 31) / (64 * WK * n_tiles)) + 1;
+  for (int first = 0; first < m_tiles; first += most) {
+    const int here = m_tiles - first < most ? m_tiles - first : most;
+    linear_split_kernel<MW, NT, WK, D, PACKED><<<(unsigned)(n_tiles * here), 64 * WK, 0, stream>>>(a, (int)n_tiles, first);
+  }
 }
 
 hipError_t launch_linear(LinearArgs a, hipStream_t stream) {

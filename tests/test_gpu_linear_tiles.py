@@ -79,3 +79,12 @@ def test_other_weights_in_turn():
     for _ in range(3):
         for (w, x), y in zip(layers, want):
             assert torch.equal(y, mx.linear(x, w.Bw, w.Bs, w.N))
+
+
+def test_residual_in_place():
+    w = Matrix(5, 4112, 96)
+    x = rows(6, 2100, 96)
+    stream = rows(7, 2100, 4112)
+    want, _ = linear_limit(x, w.values, "bf16", residual=stream.clone())
+    assert mx.linear(x, w.Bw, w.Bs, 4112, residual=stream, out=stream) is stream
+    assert_within(stream, want, "y")
