@@ -44,10 +44,8 @@ __device__ __forceinline__ u32x4 bf16_of_codes(uint32_t w, float scale) {
 
 // Place of 16-byte chunk c in row j of an LDS tile of `row_bytes` a row (a
 // multiple of 256) that is written row by row and read turned.  LDS has 64 banks
-// of 4 bytes, a turned read takes 32 lanes at once, 64 bytes of each of 4 rows, and
-// a write 8 lanes, one chunk of each of 8 rows: either lies in banks of its own.
-// (With the 4 rows 32 bytes apart instead, every turned read took twice its
-// cycles.)
+// of 4 bytes; a turned read takes 32 lanes at once, 64 bytes of each of 4 rows, which
+// lie in banks of their own so.  (32 bytes apart, they made twice the conflicts.)
 __device__ __forceinline__ constexpr int turn_swizzle(int j) { return ((j & 3) << 2) | ((j >> 2) & 1); }
 __device__ __forceinline__ int turned_at(int j, int c, int row_bytes) {
   return j * row_bytes + ((c ^ turn_swizzle(j)) << 4);
@@ -59,13 +57,23 @@ __device__ __forceinline__ constexpr int line_swizzle(int row) { return (row >> 
 // taken in two halves of two 16-deep steps.
 //   P  goes through LDS as it is, written by the memory system: a ring of three
 //      stages, loaded two stages ahead, whole 128-byte lines of its rows.
-//   T  comes as codes, three halves ahead; each lane turns its 32 or 16 codes of
-//      one row into bf16 and writes them to one of two
-//      LDS tiles, a half ahead of their use.  So every code is converted once a
-//      workgroup, and the turned reads give the operand's eight j of one k.
+//   T  comes as codes, three halves ahead; each lane turns its 16 codes of one
+//      row into bf16 and writes them to one of two LDS tiles, a half ahead of their
+//      use.  So every code is converted once a workgroup, and the turned reads give
+//      the operand's eight j of one k.
 // The operands of a step are read while the step before multiplies; the one
 // barrier of a half stands between its two steps, after which the next half's
 // T and the next stage's P are there and the places of the last ones are free.
+//
+// 256 x 256 tiles with 8 waves, 8192 x 16384 x 4096: 790 us, 1.39 PFLOP/s, and
+// transposed to f32 820 and 17 for the rows' quantization, 1.31 PFLOP/s; the
+// library's bf16 product of these sizes takes 692 to 800.  Power bounds it: the
+// matrix units are busy 75 % of the time at 1.88 GHz, and operands of zeros take
+// 592 us.  P as the instruction's first operand takes 2.5 % less than T.  With 4
+// waves of 128 x 128 outputs 840 us; waves 2 x 4 over i x k or 4 x 2: 806 and 808, and
+// transposed 876 and 866.
+// 128 x 128 tiles with 4 waves, where those are too few: 0.62 us a stage of which
+// the products are 0.21; the latency of a stage's reads bounds it.
 template <int BI, int BK, int W, int WI, bool TRANSPOSED>
 __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradProductArgs a, int i_tiles,
                                                                                      int k_tiles) {
@@ -379,7 +387,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void grad_product_kernel(const GradP
 }
 
 // Few rows of P (32 * FI at most): reading T bounds it, and nothing waits at a
-// barrier before the sums.  64 columns a workgroup; its waves and the splits
+// barrier before the sums.  24 rows of 4096 x 4096: 5.3 us and 1.7 for the splits'
+// sums; 256 x 256 tiles took 21.  64 columns a workgroup; its waves and the splits
 // take every 32 of j in turn, D of them loaded ahead.  A lane turns one chunk of
 // 32 codes into bf16 in its wave's own 4 KiB of LDS, P's rows go straight to
 // registers.  The waves' sums meet in LDS, in wave order.
