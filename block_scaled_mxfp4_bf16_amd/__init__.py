@@ -808,14 +808,14 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
     return out if z is None and not isinstance(pre, torch.Tensor) else (out, pre)
 
 
-def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias: bool = False, out=None, stream=None,
-                    workspace=None):
+def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias=False, out=None, stream=None, workspace=None):
     """The gradient of z in linear, bf16 [M, N], from that of y.
 
     dy [M, columns of y], bf16, f16 or f32, with contiguous rows; pre the z
     that linear kept (None where it has neither activation nor gate, when z is
-    not read).  bias: returns (dz, dbias), dbias f32 [N] the sum of the rows of
-    dz, formed before dz is rounded.  out may be pre itself.
+    not read).  bias: True, or an f32 [N] tensor to fill: returns (dz, dbias),
+    dbias the sum of the rows of dz, formed before dz is rounded.  out may be pre
+    itself.
     workspace: as for gemm_grouped, of mxfp4_linear_grad_pre_workspace_bytes(M, N)
     bytes; without bias none is needed."""
     L = _lib if _torch else _start()
@@ -838,7 +838,10 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias: bool = 
         _bf16(out, "out")
     out, _, ld_dz = _output(out, M, N, torch.bfloat16, dy, dev, stream)
     db = None
-    if bias:
+    if isinstance(bias, torch.Tensor):
+        db = bias
+        _array(db, torch.float32, "bias", N, dev)
+    elif bias:
         db = (torch.empty if stream is None else _allocator(stream))((N,), dtype=torch.float32, device=dy.device)
     if workspace is not None:
         ws, ws_bytes = _workspace(workspace, dev)
@@ -848,7 +851,7 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias: bool = 
                                  _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_linear_grad_pre")
-    return (out, db) if bias else out
+    return out if db is None else (out, db)
 
 
 def linear_grad_input(dz, Bw, Bs, K: int, out=None, out_dtype=None, stream=None, workspace=None):

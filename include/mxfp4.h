@@ -440,6 +440,7 @@ MXFP4_API mxfp4_status_t mxfp4_moe_combine(const void *y, int y_type, int64_t ld
 /* whose ..._workspace_bytes is 0 needs none.  Sums are f32 in an order that */
 /* the sizes of the call fix, so results are the same every time; every      */
 /* output is rounded once, to nearest even.                                   */
+/* Outputs overlap neither inputs nor each other unless it is said below.     */
 /* Limits of all of them: UNSUPPORTED for K % 32 != 0, N % 16 != 0, gated    */
 /* with N % 32 != 0, M or N > 2^20, K > 2^17, a prepared matrix beyond 2^31   */
 /* bytes, a row stride > 2^20 elements.                                       */

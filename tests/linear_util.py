@@ -5,7 +5,7 @@ import numpy as np
 import torch
 
 import oracle
-from expert_util import HALF_STEP, SMALLEST, bf16_bits, dequant, dtype_of
+from tests.expert_util import HALF_STEP, SMALLEST, bf16_bits, dequant, dtype_of
 
 ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
 

@@ -8,8 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import block_scaled_mxfp4_bf16_amd as mx
-from expert_util import HALF_STEP
-from linear_util import act, act_error, assert_within, quantized, rounded, rows, sum_error
+from tests.expert_util import HALF_STEP
+from tests.linear_util import act, act_error, assert_within, quantized, rounded, rows, sum_error
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, os.path.join(ROOT, "examples"))

@@ -5,8 +5,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import block_scaled_mxfp4_bf16_amd as mx
-from expert_util import dtype_of
-from linear_util import ACTS, Matrix, assert_within, grad_pre_limit, product_limit, quantized, rows
+from tests.expert_util import dtype_of
+from tests.linear_util import ACTS, Matrix, assert_within, grad_pre_limit, product_limit, quantized, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,14 @@ def test_grad_pre_sizes(M, cols, gated):
         assert_within(dz, want_dz, "dz of %s" % activation)
         assert_within(db, want_db, "dbias of %s" % activation)
         assert torch.equal(dz, mx.linear_grad_pre(dy, z, activation=activation, gated=gated))
+
+
+def test_grad_pre_into_a_given_dbias():
+    dy = rows(1, 700, 96, "f32", 0.1)
+    want = mx.linear_grad_pre(dy, None, bias=True)[1]
+    db = torch.full((96,), 7.0, device="cuda")
+    assert mx.linear_grad_pre(dy, None, bias=db)[1] is db
+    assert torch.equal(db, want)
 
 
 @pytest.mark.parametrize("t", TYPES)

@@ -4,8 +4,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import block_scaled_mxfp4_bf16_amd as mx
-from expert_util import dtype_of
-from linear_util import ACTS, Matrix, assert_within, linear_limit, rows
+from tests.expert_util import dtype_of
+from tests.linear_util import ACTS, Matrix, assert_within, linear_limit, rows
 
 pytestmark = pytest.mark.gpu
 

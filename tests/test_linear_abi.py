@@ -134,6 +134,8 @@ BW, BS = cpu(2, 512, dtype=torch.uint8), cpu(8, 256, dtype=torch.uint8)  # [32, 
     (lambda: mx.linear_grad_pre(cpu(4, 32), cpu(4, 32, dtype=torch.float32), activation="silu"), "pre must be bf16"),
     (lambda: mx.linear_grad_pre(cpu(4, 32), cpu(4, 32), out=cpu(4, 32, dtype=torch.float32)), "out must be bf16"),
     (lambda: mx.linear_grad_pre(cpu(4, 32, requires_grad=True), None), "dy requires gradients"),
+    (lambda: mx.linear_grad_pre(cpu(4, 32), None, bias=cpu(32)), "bias"),
+    (lambda: mx.linear_grad_pre(cpu(4, 32), None, bias=cpu(31, dtype=torch.float32)), "bias"),
     (lambda: mx.linear_grad_pre(cpu(4, 32), None), "cuda tensors"),
     (lambda: mx.linear_grad_input(cpu(4, 32), BW, BS, 96), "prepared"),
     (lambda: mx.linear_grad_input(cpu(4, 32, dtype=torch.float32), BW, BS, 64), "dz must be bf16"),
