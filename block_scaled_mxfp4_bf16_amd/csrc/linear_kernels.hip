@@ -4,6 +4,7 @@
 //
 // The rows are quantized into the prepared layout by a launch of their own,
 // so that both operands of the product are read as whole blocks.
+#include "linear_bounds.hpp"
 #include "linear_epilogue.hpp"
 #include "linear_internal.hpp"
 
@@ -114,6 +115,7 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
       gw[nt] = n_tile * NT + nt;
       gok[nt] = gw[nt] < groups;
     }
+    gw[nt] = group_within(gw[nt], groups);
   }
   v4f acc[MW][NT];
 #pragma unroll
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
   } st[D];
   auto load = [&](int q, int ks) __attribute__((always_inline)) {
     // a K chunk past the end meets zeros of the rows; it must not run past
-    // the matrix all the same
+    // the matrix all the same (its offset may pass 2^31, hence unsigned)
     const bool ok = (4 * ks + q4) * 32 < K;
     if (!PACKED)
 #pragma unroll
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       st[q].b[nt] = __builtin_amdgcn_raw_buffer_load_b128(
-          b_rsrc, off_or_oob(ok && gok[nt], gw[nt] * K * 8 + ks * 1024 + lane * 16), 0, 0);
+          b_rsrc, off_or_oob(ok && gok[nt], (int)((uint32_t)(gw[nt] * K * 8) + ks * 1024 + lane * 16)), 0, 0);
       st[q].bs[nt] = __builtin_amdgcn_raw_buffer_load_b32(
           s_rsrc, off_or_oob(ok && gok[nt], (gw[nt] >> 1) * gp * 32 + (ks >> 1) * 256 + lane * 4), 0, 0);
     }
@@ -218,10 +220,11 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
 // with them and without, rows of 4096 x 4096: 1536 (96 tiles) 39.3 and 37.5, 2048 (128)
 // 40.3 and 45.2; 4096 x 1024: 20.4 and 20.9, 20.7 and 26.5; 2048 x 2048, 2560 rows (80)
 // 28.6 and 27.1, 4096 (128) 30.9 and 35.8.  Gated ones need their pairs of column
-// groups whole.
+// groups whole.  (Of matrices within 4 KiB of 2^31 bytes their steps past K would
+// pass that.)
 static bool use_tiles(const LinearArgs &a) {
   const int64_t m_tiles = (a.M + 255) / 256, n_tiles = ((int64_t)a.N + 255) / 256;
-  return m_tiles * n_tiles >= 128 && (!a.gated || a.N % 64 == 0);
+  return m_tiles * n_tiles >= 128 && (!a.gated || a.N % 64 == 0) && tile_offsets_fit(a.N, a.K);
 }
 
 // Whether the rows are quantized on the way, in one launch: 16 of them at most,

@@ -21,6 +21,7 @@
 // lane has 8 neighbouring columns of a row and four lanes 64 bytes of bf16.  (Turned
 // in LDS, 8 rows x 64 columns a wave at a time, a tile's epilogue took 13 us for
 // the 8 us of this form, most of it waiting for LDS.)
+#include "linear_bounds.hpp"
 #include "linear_epilogue.hpp"
 #include "linear_internal.hpp"
 
@@ -76,7 +77,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave & 3, wk = wave >> 2;  // the wave's 64 rows and 128 weight rows
   const int N = a.N, K = a.K;
-  const int KS = (K + 127) >> 7, steps = (KS + 3) & ~3;  // steps past K multiply zeros
+  const int steps = tile_steps(K);  // those past K multiply zeros
   const int gp = ((K >> 5) + 7) & ~7;
   const int b_bytes = (N >> 4) * K * 8, s_bytes = ((N + 255) >> 8) * 8 * gp * 32;
 
@@ -115,12 +116,13 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(const LinearArgs a,
     u.w_size = none ? 0 : b_bytes;
     u.ws_size = none ? 0 : s_bytes;
     // the wave's blocks 2 w and 2 w + 1 of 16; gated, of each 8 blocks the first
-    // four are the gate's and the others their up rows
+    // four are the gate's and the others their up rows; past the last group that one
+    // again
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int b = 2 * wave + q;
       const int g = GATED ? ((b >> 2) & 1) * (N >> 5) + (u.n0 >> 4) + (b >> 3) * 4 + (b & 3) : (u.n0 >> 4) + b;
-      u.b_off[q] = g * K * 8;
+      u.b_off[q] = group_within(g, N >> 4) * K * 8;
     }
     const int g = GATED ? ((wave >> 1) & 1) * (N >> 6) + (u.n0 >> 5) + (wave >> 2) * 2 + (wave & 1) : (u.n0 >> 5) + wave;
     u.s_off = g * gp * 32;
