@@ -420,13 +420,18 @@ MXFP4_TYPE_BF16, MXFP4_TYPE_F16, MXFP4_TYPE_F32 = 0, 1, 2
 
 _torch = None
 _types = {}
+_forward_ad = None  # torch.autograd.forward_ad
+_increment_version = None
 
 
 def _start():
     """torch and the library, once."""
-    global _torch
+    global _torch, _forward_ad, _increment_version
     L = _load()
     import torch
+    import torch.autograd.forward_ad
+    import torch.autograd.graph
+    _forward_ad, _increment_version = torch.autograd.forward_ad, torch.autograd.graph.increment_version
     _types.update({torch.bfloat16: MXFP4_TYPE_BF16, torch.float16: MXFP4_TYPE_F16, torch.float32: MXFP4_TYPE_F32})
     _torch = torch
     return L
@@ -735,8 +740,12 @@ def _activation(name):
 
 
 def _untracked(t, what):
+    """Refuses a tensor, input or output, whose gradient or tangent autograd would lose in the call."""
     if t.requires_grad:
         _no_gradients(what, "which autograd does not follow through this call (mx.linear_grad_* compute them)")
+    # no level is open unless the caller works in forward mode; asking torch costs 0.3 us a tensor
+    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+        raise RuntimeError("%s carries a forward-mode tangent, which autograd does not follow through this call" % what)
 
 
 def _bf16(t, what):
@@ -749,6 +758,7 @@ def _output(out, rows, cols, dtype, like, dev, stream):
     if out is None:
         out = (_torch.empty if stream is None else _allocator(stream))((rows, cols), dtype=dtype, device=like.device)
         return out, _type(out), cols
+    _untracked(out, "out")
     return out, _type(out), _rows_of(out, "out", rows, cols, dev)
 
 
@@ -764,10 +774,13 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
 
     pre: a bf16 [M, N] tensor that receives z, or True for a new one; the call
     then returns (y, z), and linear_grad_pre takes z.
+    Tensors that are given to be written (here and in the gradients) count as
+    changed in place: a backward pass that saved one of them says so.
     workspace: as for gemm_grouped, of mxfp4_linear_workspace_bytes(M, N, K) bytes."""
     L = _lib if _torch else _start()
     torch = _torch
     ws, ws_bytes = None, 0
+    written = () if out is None else (out,)
     M, K, ldx, dev = _matrix(x, "x", "M, K")
     _bf16(x, "x")
     _untracked(x, "x")
@@ -793,10 +806,13 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
     z, ld_pre = None, N
     if pre is True:
         pre = (torch.empty if stream is None else _allocator(stream))((M, N), dtype=torch.bfloat16, device=x.device)
-    if pre is not None and pre is not False:
+        z = pre.data_ptr()
+    elif pre is not None and pre is not False:
         _bf16(pre, "pre")
         ld_pre = _rows_of(pre, "pre", M, N, dev)
+        _untracked(pre, "pre")
         z = pre.data_ptr()
+        written += (pre,)
     if workspace is not None:
         ws, ws_bytes = _workspace(workspace, dev)
     _on_gpu(dev)
@@ -805,6 +821,8 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
                         _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_linear")
+    if written:
+        _increment_version(written)
     return out if z is None and not isinstance(pre, torch.Tensor) else (out, pre)
 
 
@@ -821,6 +839,7 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias=False, o
     L = _lib if _torch else _start()
     torch = _torch
     ws, ws_bytes = None, 0
+    written = () if out is None else (out,)
     M, cols, ld_dy, dev = _matrix(dy, "dy", "M, columns")
     dt = _type(dy)
     _untracked(dy, "dy")
@@ -841,6 +860,8 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias=False, o
     if isinstance(bias, torch.Tensor):
         db = bias
         _array(db, torch.float32, "bias", N, dev)
+        _untracked(db, "bias")
+        written += (db,)
     elif bias:
         db = (torch.empty if stream is None else _allocator(stream))((N,), dtype=torch.float32, device=dy.device)
     if workspace is not None:
@@ -851,6 +872,8 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias=False, o
                                  _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_linear_grad_pre")
+    if written:
+        _increment_version(written)
     return out if db is None else (out, db)
 
 
@@ -862,6 +885,7 @@ def linear_grad_input(dz, Bw, Bs, K: int, out=None, out_dtype=None, stream=None,
     workspace: as for gemm_grouped, of mxfp4_linear_grad_input_workspace_bytes(M, N, K) bytes."""
     L = _lib if _torch else _start()
     ws, ws_bytes = None, 0
+    written = () if out is None else (out,)
     M, N, ld_dz, dev = _matrix(dz, "dz", "M, N")
     _bf16(dz, "dz")
     _untracked(dz, "dz")
@@ -875,6 +899,8 @@ def linear_grad_input(dz, Bw, Bs, K: int, out=None, out_dtype=None, stream=None,
                                    ws, ws_bytes, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_linear_grad_input")
+    if written:
+        _increment_version(written)
     return out
 
 
@@ -886,6 +912,7 @@ def linear_grad_weight(dz, x, out=None, out_dtype=None, stream=None, workspace=N
     workspace: as for gemm_grouped, of mxfp4_linear_grad_weight_workspace_bytes(M, N, K) bytes."""
     L = _lib if _torch else _start()
     ws, ws_bytes = None, 0
+    written = () if out is None else (out,)
     M, N, ld_dz, dev = _matrix(dz, "dz", "M, N")
     _bf16(dz, "dz")
     _untracked(dz, "dz")
@@ -902,4 +929,6 @@ def linear_grad_weight(dz, x, out=None, out_dtype=None, stream=None, workspace=N
                                     ws_bytes, _current_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc, "mxfp4_linear_grad_weight")
+    if written:
+        _increment_version(written)
     return out
