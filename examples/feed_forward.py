@@ -26,6 +26,8 @@ class _Block(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        if torch.is_grad_enabled():  # create_graph: what is returned would be cut off from x without a word
+            raise RuntimeError("the block has no gradients of gradients")
         x, h, z = ctx.saved_tensors
         block, dy = ctx.block, dy.contiguous()
         up, down = ctx.matrices
