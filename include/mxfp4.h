@@ -509,6 +509,9 @@ MXFP4_API mxfp4_status_t mxfp4_linear_grad_input(const void *dz, int64_t ld_dz, 
                                                  mxfp4_stream_t stream);
 
 /* The gradient of W: dw[n, k] = sum_m dz[m, n] * Q(x)[m, k].                  */
+/* As above, a value of 2^128 counts as infinite: in Q(x) that of an element   */
+/* of 1.75 * 2^127 and more, as scale byte 253 rounds it.  It touches its own   */
+/* column of dw only, also where dz is 0.                                       */
 /*   dz  [M, N] bf16, ld_dz apart;  x  [M, K] bf16, ldx apart, finite (input) */
 /*   dw  [N, K] of dw_type, ld_dw apart                             (output) */
 /* M may be 0: dw is then zero.                                                */
