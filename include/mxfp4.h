@@ -462,7 +462,9 @@ typedef enum {
 /*   y         [M, N] (gated: [M, N/2]) of y_type, ldy apart        (output) */
 /*   pre       [M, N] bf16, ld_pre apart, or NULL: receives z, which the     */
 /*             gradient of the activation takes                     (output) */
-/* The activation takes the f32 z.  M may be 0.  x must be finite.            */
+/* The activation takes the f32 z.  M may be 0.  x must be finite; infinities */
+/* and NaN in bias and residual touch their own column and element, with what */
+/* the formulas above give (silu and gelu of -infinity are NaN).              */
 /* Errors: INVALID_ARG (null, M < 0, N or K < 1, unknown type or activation, */
 /*         a row stride smaller than the row, x or its row stride not        */
 /*         16-byte aligned, B not 16-byte aligned, another pointer not        */
@@ -478,7 +480,9 @@ MXFP4_API mxfp4_status_t mxfp4_linear(const void *x, int64_t ldx, const void *Bq
 /*   dz = dy * f'(pre)                                                        */
 /*   dz = [dy * up * f'(gate), dy * f(gate)], pre = [gate, up]    (gated)      */
 /*   dbias[n] = sum over the rows of dz[:, n], before dz is rounded           */
-/* The slope of relu at 0 is 0.                                               */
+/* The slope of relu at 0 is 0, and at NaN.  Infinities and NaN in dy and pre  */
+/* touch their own element of dz (gated: both of its halves) and its column of  */
+/* dbias; the other slopes at infinities and NaN are NaN.                       */
 /*   dy     [M, y's columns] of dy_type, ld_dy apart                (input)  */
 /*   pre    [M, N] bf16, ld_pre apart, as mxfp4_linear left it; not read, and */
 /*          may be NULL, for MXFP4_ACT_NONE without gate             (input)  */
