@@ -219,12 +219,15 @@ __global__ __launch_bounds__(64 * WK) void linear_split_kernel(const LinearArgs 
 // Whether 256 x 256 tiles are the faster form: one for half of the CUs.  us a call
 // with them and without, rows of 4096 x 4096: 1536 (96 tiles) 39.3 and 37.5, 2048 (128)
 // 40.3 and 45.2; 4096 x 1024: 20.4 and 20.9, 20.7 and 26.5; 2048 x 2048, 2560 rows (80)
-// 28.6 and 27.1, 4096 (128) 30.9 and 35.8.  Gated ones need their pairs of column
+// 28.6 and 27.1, 4096 (128) 30.9 and 35.8; 16384 x 4096, 264 rows (128) 40.6 and 35.0,
+// 384 (128) 40.7 and 41.5, 512 (128) 41.5 and 51.  Few rows of very many columns leave
+// the tiles almost empty (tiles_filled).  Gated ones need their pairs of column
 // groups whole.  (Of matrices within 4 KiB of 2^31 bytes their steps past K would
 // pass that.)
 static bool use_tiles(const LinearArgs &a) {
   const int64_t m_tiles = (a.M + 255) / 256, n_tiles = ((int64_t)a.N + 255) / 256;
-  return m_tiles * n_tiles >= 128 && (!a.gated || a.N % 64 == 0) && tile_offsets_fit(a.N, a.K);
+  return m_tiles * n_tiles >= 128 && tiles_filled(a.M, a.N) && (!a.gated || a.N % 64 == 0) &&
+         tile_offsets_fit(a.N, a.K);
 }
 
 // Whether the rows are quantized on the way, in one launch: 16 of them at most,

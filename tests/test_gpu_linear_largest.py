@@ -43,9 +43,9 @@ def largest():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("M", [1, 20, 40])
+@pytest.mark.parametrize("M", [1, 20, 80])
 def test_layer(largest, M):
-    """One row quantized on the way; more in the large tiles, the last of which ends within 256 columns."""
+    """One row quantized on the way, 20 before; 80 in the large tiles, the last of which ends within 256 columns."""
     x = rows(5, M, K)
     y = mx.linear(x, largest.Bw, largest.Bs, N)
     q = quantized(x)
