@@ -100,8 +100,8 @@ __global__ __launch_bounds__(256) void sum_chunks_kernel(const float *partial, i
   out[i] = v;
 }
 
-// Rows of a chunk: enough chunks to fill the chip, no more than 128 of them.
-static int64_t rows_per_chunk(int64_t M) { return M <= 512 ? 16 : (M + 127) / 128 < 16 ? 16 : (M + 127) / 128; }
+// Rows of a chunk: 16, four a wave, until there are 128 chunks, then more.
+static int64_t rows_per_chunk(int64_t M) { return M <= 2048 ? 16 : (M + 127) / 128; }
 
 size_t grad_pre_workspace_bytes(int64_t M, int64_t N) {
   const int64_t rows = rows_per_chunk(M);

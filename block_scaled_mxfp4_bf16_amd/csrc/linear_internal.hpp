@@ -32,7 +32,6 @@ struct LinearArgs {
   uint16_t *pre;  // or null
   int64_t ld_pre;
   int M, N, K, sw;
-  int64_t ws_bytes;
   uint8_t *ws;
   // set by launch_linear
   uint8_t *codes, *scales;  // of the quantized rows, in ws

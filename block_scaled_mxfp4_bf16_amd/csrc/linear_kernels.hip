@@ -2,8 +2,9 @@
 //   z = Q(x) * B^T + bias,  y = f(z) + residual,
 // or, gated, y = f(first half of z's columns) * second half + residual.
 //
-// The rows are quantized into the prepared layout by a launch of their own,
-// so that both operands of the product are read as whole blocks.
+// More than a few rows are quantized into the prepared layout by a launch of
+// their own, so that both operands of the product are read as whole blocks; a
+// few are quantized by the product's waves themselves (in_one_launch).
 #include "linear_bounds.hpp"
 #include "linear_epilogue.hpp"
 #include "linear_internal.hpp"
