@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import types
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # MXFP4_LIB may point at another build of the same library (e.g. a debug build).
@@ -420,7 +421,7 @@ MXFP4_TYPE_BF16, MXFP4_TYPE_F16, MXFP4_TYPE_F32 = 0, 1, 2
 
 _torch = None
 _types = {}
-_forward_ad = None  # torch.autograd.forward_ad
+_forward_ad = None  # its _current_level is negative unless the caller works in forward mode
 _increment_version = None
 
 
@@ -431,7 +432,11 @@ def _start():
     import torch
     import torch.autograd.forward_ad
     import torch.autograd.graph
-    _forward_ad, _increment_version = torch.autograd.forward_ad, torch.autograd.graph.increment_version
+    _forward_ad = torch.autograd.forward_ad
+    if not hasattr(_forward_ad, "_current_level"):
+        _forward_ad = types.SimpleNamespace(_current_level=0, unpack_dual=_forward_ad.unpack_dual)  # asks each tensor
+    # without the isinstance of the public one, where there is it
+    _increment_version = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
     _types.update({torch.bfloat16: MXFP4_TYPE_BF16, torch.float16: MXFP4_TYPE_F16, torch.float32: MXFP4_TYPE_F32})
     _torch = torch
     return L
@@ -739,13 +744,17 @@ def _activation(name):
     return kind
 
 
-def _untracked(t, what):
-    """Refuses a tensor, input or output, whose gradient or tangent autograd would lose in the call."""
-    if t.requires_grad:
-        _no_gradients(what, "which autograd does not follow through this call (mx.linear_grad_* compute them)")
-    # no level is open unless the caller works in forward mode; asking torch costs 0.3 us a tensor
-    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
-        raise RuntimeError("%s carries a forward-mode tangent, which autograd does not follow through this call" % what)
+def _tracked(what):
+    """A tensor, input or output, requires gradients: refused where autograd would follow it."""
+    _no_gradients(what, "which autograd does not follow through this call (mx.linear_grad_* compute them)")
+
+
+def _no_tangents(**tensors):
+    """Refuses tensors that carry a tangent; `requires_grad` does not show it.  Asking costs 0.3 us a tensor, so
+    callers look at the level first."""
+    for what, t in tensors.items():
+        if isinstance(t, _torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError("%s carries a forward-mode tangent, which autograd does not follow through this call" % what)
 
 
 def _bf16(t, what):
@@ -758,7 +767,8 @@ def _output(out, rows, cols, dtype, like, dev, stream):
     if out is None:
         out = (_torch.empty if stream is None else _allocator(stream))((rows, cols), dtype=dtype, device=like.device)
         return out, _type(out), cols
-    _untracked(out, "out")
+    if out.requires_grad:
+        _tracked("out")
     return out, _type(out), _rows_of(out, "out", rows, cols, dev)
 
 
@@ -781,9 +791,12 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
     torch = _torch
     ws, ws_bytes = None, 0
     written = () if out is None else (out,)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x=x, bias=bias, residual=residual, pre=pre, out=out)
     M, K, ldx, dev = _matrix(x, "x", "M, K")
     _bf16(x, "x")
-    _untracked(x, "x")
+    if x.requires_grad:
+        _tracked("x")
     kind = _activation(activation)
     if _prepared(Bw, Bs, N, K, dev) != 1:
         raise ValueError("Bw and Bs must hold one matrix")
@@ -792,7 +805,8 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
     if bias is not None:
         bias_type = _type(bias)
         _array(bias, bias.dtype, "bias", N, dev)
-        _untracked(bias, "bias")
+        if bias.requires_grad:
+            _tracked("bias")
         bias = bias.data_ptr()
     out, yt, ldy = _output(out, M, cols, out_dtype or (torch.bfloat16 if residual is None else residual.dtype), x, dev,
                            stream)
@@ -801,7 +815,8 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
         ld_res = _rows_of(residual, "residual", M, cols, dev)
         if residual.dtype != out.dtype:
             raise TypeError("residual is %s, out %s" % (residual.dtype, out.dtype))
-        _untracked(residual, "residual")
+        if residual.requires_grad:
+            _tracked("residual")
         residual = residual.data_ptr()
     z, ld_pre = None, N
     if pre is True:
@@ -810,7 +825,8 @@ def linear(x, Bw, Bs, N: int, bias=None, activation=None, gated: bool = False, r
     elif pre is not None and pre is not False:
         _bf16(pre, "pre")
         ld_pre = _rows_of(pre, "pre", M, N, dev)
-        _untracked(pre, "pre")
+        if pre.requires_grad:
+            _tracked("pre")
         z = pre.data_ptr()
         written += (pre,)
     if workspace is not None:
@@ -840,16 +856,20 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias=False, o
     torch = _torch
     ws, ws_bytes = None, 0
     written = () if out is None else (out,)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(dy=dy, pre=pre, bias=bias, out=out)
     M, cols, ld_dy, dev = _matrix(dy, "dy", "M, columns")
     dt = _type(dy)
-    _untracked(dy, "dy")
+    if dy.requires_grad:
+        _tracked("dy")
     kind = _activation(activation)
     N = 2 * cols if gated else cols
     z, ld_pre = None, N
     if pre is not None:
         _bf16(pre, "pre")
         ld_pre = _rows_of(pre, "pre", M, N, dev)
-        _untracked(pre, "pre")
+        if pre.requires_grad:
+            _tracked("pre")
         z = pre.data_ptr()
     elif kind or gated:
         raise ValueError("an activation or a gate needs pre")
@@ -860,7 +880,8 @@ def linear_grad_pre(dy, pre, activation=None, gated: bool = False, bias=False, o
     if isinstance(bias, torch.Tensor):
         db = bias
         _array(db, torch.float32, "bias", N, dev)
-        _untracked(db, "bias")
+        if db.requires_grad:
+            _tracked("bias")
         written += (db,)
     elif bias:
         db = (torch.empty if stream is None else _allocator(stream))((N,), dtype=torch.float32, device=dy.device)
@@ -886,9 +907,12 @@ def linear_grad_input(dz, Bw, Bs, K: int, out=None, out_dtype=None, stream=None,
     L = _lib if _torch else _start()
     ws, ws_bytes = None, 0
     written = () if out is None else (out,)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(dz=dz, out=out)
     M, N, ld_dz, dev = _matrix(dz, "dz", "M, N")
     _bf16(dz, "dz")
-    _untracked(dz, "dz")
+    if dz.requires_grad:
+        _tracked("dz")
     if _prepared(Bw, Bs, N, K, dev) != 1:
         raise ValueError("Bw and Bs must hold one matrix")
     out, xt, ld_dx = _output(out, M, K, out_dtype or _torch.bfloat16, dz, dev, stream)
@@ -913,14 +937,18 @@ def linear_grad_weight(dz, x, out=None, out_dtype=None, stream=None, workspace=N
     L = _lib if _torch else _start()
     ws, ws_bytes = None, 0
     written = () if out is None else (out,)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(dz=dz, x=x, out=out)
     M, N, ld_dz, dev = _matrix(dz, "dz", "M, N")
     _bf16(dz, "dz")
-    _untracked(dz, "dz")
+    if dz.requires_grad:
+        _tracked("dz")
     rows, K, ldx, x_dev = _matrix(x, "x", "M, K")
     if rows != M or x_dev != dev:
         raise ValueError("x must have dz's %d rows on %s" % (M, _device(dev)))
     _bf16(x, "x")
-    _untracked(x, "x")
+    if x.requires_grad:
+        _tracked("x")
     out, wt, ld_dw = _output(out, N, K, out_dtype or _torch.float32, dz, dev, stream)
     if workspace is not None:
         ws, ws_bytes = _workspace(workspace, dev)
