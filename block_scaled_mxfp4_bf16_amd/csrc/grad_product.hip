@@ -71,7 +71,8 @@ __device__ __forceinline__ constexpr int line_swizzle(int row) { return (row >> 
 // matrix units are busy 75 % of the time at 1.88 GHz, and operands of zeros take
 // 592 us.  P as the instruction's first operand takes 2.5 % less than T.  With 4
 // waves of 128 x 128 outputs 840 us; waves 2 x 4 over i x k or 4 x 2: 806 and 808, and
-// transposed 876 and 866.
+// transposed 876 and 866.  One tile a workgroup and CU: a last round that is not full
+// costs as much as one that is (k 4160 for 4096, 544 tiles for 512: 1034 us for 798).
 // 128 x 128 tiles with 4 waves, where those are too few: 0.62 us a stage of which
 // the products are 0.21; the latency of a stage's reads bounds it.
 template <int BI, int BK, int W, int WI, bool TRANSPOSED>

@@ -233,10 +233,11 @@ static bool use_tiles(const LinearArgs &a) {
 
 // Whether the rows are quantized on the way, in one launch: 16 of them at most,
 // and as every workgroup reads all of them, 192 KiB.  us so and with a launch of
-// their own, captured: 13 rows of 4096 x 4096 6.3 and 6.4; 2112 x 7168, 2 rows 6.3
-// and 7.5, 8 rows 7.8 and 7.6, 13 rows 8.9 and 7.4; 13 rows of 4096 x 1024 4.6 and
-// 5.8.  A call that is not captured pays 2 us more for the second launch: the 13
-// rows of 2112 x 7168 take 9.6 and 10.6.
+// their own, captured and not: 16 rows of 4096 x 4096 6.8 and 7.1, 7.9 and 11; 2112 x
+// 7168, 2 rows 6.2 and 7.9, 7.5 and 11, 8 rows 7.9 and 7.8, 7.8 and 11, 13 rows 8.8 and
+// 7.8, 8.5 and 11, 16 rows 9.8 and 7.9, 9.5 and 11; 16384 x 4096, 16 rows 10.5 and
+// 11.7, 10.3 and 11.5.  Captured calls would rather change at an M * K of 65536, others
+// beyond 114688: the bound follows the others and costs captured ones 1 us at most.
 static bool in_one_launch(int64_t M, int64_t K) { return M <= 16 && M * K <= 98304; }
 
 size_t linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return in_one_launch(M, K) ? 0 : packed_bytes(M, K); }

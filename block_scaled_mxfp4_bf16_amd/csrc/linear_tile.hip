@@ -14,9 +14,10 @@
 //
 // A step takes 0.7 to 0.8 us, of which the matrix units work 0.43 at 2.4 GHz and 0.5
 // at the clock that they leave; without its loads it takes 0.67, without its products
-// 0.43.  8192 x 4096 x 8192 with residual: 154 us; gated 8192 x 16384 x 4096 with z kept:
-// 277, where 402 MB of outputs, written by all CUs at a time, take a third.  Starting
-// the CUs up to 11 us apart so that these bursts spread changed nothing.
+// 0.43.  Median launches: 8192 x 4096 x 8192 with residual 158 us (least 154); gated
+// 8192 x 16384 x 4096 with z kept 292 (277), where 402 MB of outputs, written by all
+// CUs at a time, take a third, and up to 330 by where the buffers lie.  Starting the CUs
+// up to 11 us apart so that these bursts spread changed nothing.
 // The sums of two neighbouring blocks change places between lanes, after which a
 // lane has 8 neighbouring columns of a row and four lanes 64 bytes of bf16.  (Turned
 // in LDS, 8 rows x 64 columns a wave at a time, a tile's epilogue took 13 us for
